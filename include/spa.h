@@ -470,6 +470,117 @@ spa_status spa_pbs_prefill_timed(const spa_pbs_args* a, void* ws, size_t ws_byte
                                  void* const* events);
 
 /* ------------------------------------------------------------------------------------
+ * Paged KV cache, in bf16 or in 4 bits (interface additions; the method pages keep K and V
+ * dense).  A pool of pages of `page` tokens; page_table[b][i] names the page that holds
+ * tokens [i * page, (i + 1) * page) of sequence b, and kv_len[b] counts its tokens, the new
+ * ones of a call included, so one array serves append, attend and gather.
+ *   SPA_KV_BF16  data [num_pages, Hkv, page, 2, d] bf16: a token's key, then its value
+ *   SPA_KV_INT4  data [num_pages, Hkv, page, d + 16] bytes: d/2 bytes of key codes, d/2 of
+ *                value codes, 4 bf16 key scales, 4 bf16 value scales.  A row of d values has 4
+ *                groups of d/4 consecutive channels; a value is scale * (code - 8), scale >= 0
+ *                (or NaN: a group that held a value that was not finite).  Of group g, channel
+ *                j (0 .. d/4 - 1):
+ *                  keys   byte (j / (d/16)) * d/8 + g * d/32 + (j % (d/16)) / 2, low nibble for
+ *                         even j, high for odd
+ *                  values byte (j % 8) * d/16 + g * d/64 + j / 16, low nibble for j % 16 < 8
+ * spa_paged_row_bytes gives a token's bytes per kv head: 4 d (bf16) or d + 16.
+ * d in {64, 128}; page a power of two, 16 .. 1024; data 16-byte aligned.  page_table
+ * [B, max_pages] and kv_len [B] are int32 in device memory, read when the kernels run.
+ * seq_start [B + 1] int32, device memory: the new tokens (rows of q, k, v, out) of sequence b
+ * are rows [seq_start[b], seq_start[b + 1]), the last of them token kv_len[b] - 1; rows before
+ * seq_start[0] or from seq_start[B] on belong to nobody: they are not read, and what they
+ * would be written to stays as it is.  NULL: one new token per sequence, T = B.
+ * Device-side conditions raise (1 << SPA_ERR_INVALID_ARG) in the status word at the head of
+ * ws: a page number outside [0, num_pages), a length outside [0, max_pages * page], a sequence
+ * start out of order.  A token on a bad page is neither written nor attended to.
+ */
+typedef enum spa_kv_format { SPA_KV_BF16 = 0, SPA_KV_INT4 = 1 } spa_kv_format;
+
+typedef struct spa_paged_kv {
+    int format;                 /* spa_kv_format */
+    int num_pages, Hkv, page, d;
+    int B, max_pages;
+    void* data;
+    const int32_t* page_table;
+    const int32_t* kv_len;
+} spa_paged_kv;
+
+size_t spa_paged_row_bytes(int format, int d);   /* 0 for an unknown format */
+
+/* Appends T new tokens, rotating queries and keys on the way:
+ *   for pair i of the rot / 2 rotated channel pairs (c, c'): a = pos * inv_freq[i],
+ *   x[c] cos a - x[c'] sin a and x[c'] cos a + x[c] sin a replace x[c] and x[c'];
+ *   (c, c') = (i, i + rot / 2), or (2 i, 2 i + 1) with interleaved != 0; channels from rot on
+ *   stay.  pos is the token's place in the cache, or positions[t].  The angle is computed in
+ *   binary64, the rotation in binary32.
+ *   k, v   [T, Hkv, d] bf16 with the given token and head strides (elements, multiples of 8;
+ *          slices of a fused projection need no copy); 16-byte aligned
+ *   q      [T, Hq, d] likewise, or NULL; q_out [T, Hq, d] bf16 dense, must not overlap q, k or v
+ *   4-bit rows: the scale is amax / 7 of the group rounded up to bf16, the code the nearest
+ *   (even) integer to x / scale plus 8, from the keys as rotated (not rounded to bf16 first), so
+ *   |x - value| <= scale / 2 up to binary32 rounding.
+ * Two tokens of one call that name the same slot leave either of them.  rot a multiple of 16,
+ * 0 .. d (0: no rotation, inv_freq unused).  ws NULL (no status word) or >= 256 bytes. */
+typedef struct spa_paged_append_args {
+    spa_paged_kv kv;
+    int T, Hq;
+    const int32_t* seq_start;   /* [B + 1] or NULL */
+    const int32_t* positions;   /* [T] or NULL */
+    const uint16_t* k;
+    const uint16_t* v;
+    const uint16_t* q;          /* or NULL */
+    int64_t k_token_stride, k_head_stride, v_token_stride, v_head_stride, q_token_stride, q_head_stride;
+    uint16_t* q_out;
+    const float* inv_freq;      /* [rot / 2], device memory */
+    int rot, interleaved;
+} spa_paged_append_args;
+
+spa_status spa_paged_append(const spa_paged_append_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* Reads rows back as dense bf16, the layout of the dense kernels: token start[b] + i of sequence
+ * b to K, V [B, Hkv, N, d] row i, for 0 <= i < N below kv_len[b]; other rows stay as they are.
+ * start [B] int32 or NULL (0).  K, V 16-byte aligned.  4-bit values are scale * (code - 8)
+ * rounded once.  ws NULL or >= 256 bytes. */
+typedef struct spa_paged_gather_args {
+    spa_paged_kv kv;
+    int N;
+    const int32_t* start;
+    uint16_t* K;
+    uint16_t* V;
+} spa_paged_gather_args;
+
+spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_bytes, void* stream);
+
+/* Exact softmax attention of the new tokens over the cache: out[t][h] = softmax(sm_scale q K^T) V.
+ *   idx NULL: the i-th of sequence b's n new tokens sees tokens [0, kv_len[b] - n + i] (causal).
+ *   idx, count: one query per sequence (T = B, seq_start NULL), restricted to supports as
+ *   spa_sparse_attend takes them: [U, cap] and [U], entry e covers tokens [e * unit_tokens,
+ *   (e + 1) * unit_tokens) below kv_len[b]; U = B * Hkv (collapse GROUP_MEAN) or B * Hq (NONE).
+ *   q [T, Hq, d] bf16 with token and head strides (elements, multiples of 8), 16-byte aligned;
+ *   out [T, Hq, d] bf16, out_f32 [T, Hq, d] fp32 (optional), lse [T, Hq] fp32 (optional).
+ * A query that sees nothing gives out = 0 and lse = -inf.  Weights are carried in 11 bits (4-bit
+ * cache: fp16 against exact codes) or about 16 (bf16 cache), sums in binary32.  What a
+ * query does not see does not reach it, values that are not finite included.
+ * Hq / Hkv <= 16; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(d). */
+typedef struct spa_paged_attend_args {
+    spa_paged_kv kv;
+    int T, Hq;
+    const int32_t* seq_start;
+    const uint16_t* q;
+    int64_t q_token_stride, q_head_stride;
+    const int32_t* idx;
+    const int32_t* count;
+    int cap, collapse, unit_tokens;
+    float sm_scale;
+    uint16_t* out;
+    float* out_f32;
+    float* lse;
+} spa_paged_attend_args;
+
+spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_bytes, void* stream);
+size_t spa_paged_attend_workspace_bytes(int d);   /* depends on the current device's SM count */
+
+/* ------------------------------------------------------------------------------------
  * Device status word of a workspace (sticky OR of SPA_ERR_* bits as (1 << code)).
  * Synchronises `stream`, copies the word to *bits and, if reset != 0, clears it.
  * Returns SPA_OK or SPA_ERR_CUDA.

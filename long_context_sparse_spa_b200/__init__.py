@@ -20,6 +20,7 @@ import torch
 from ._abi import (SPA_COLLAPSE_GROUP_MEAN, SPA_COLLAPSE_NONE, SPA_DECODE_AUTO, SPA_DECODE_FUSED, SPA_DECODE_SEPARATE,
                    SPA_SCORE_LOWRANK, SPA_SCORE_MEAN_BLOCK,
                    SPA_SCORE_MINMAX_BLOCK, SPA_SCORE_TAYLOR_BLOCK, SPA_SELECT_TOPK, SPA_STATS_BF16, SPA_SELECT_TOPP, SpaDecodeArgs, SpaError, SpaPbsArgs, SpaPrefillArgs, check, lib, lib_path)
+from ._abi import SPA_KV_BF16, SPA_KV_INT4, SpaPagedAppendArgs, SpaPagedAttendArgs, SpaPagedGatherArgs, SpaPagedKv
 
 __all__ = [
     "SpaError", "lib", "lib_path", "block_stats", "index_scores", "select_topk", "select_topp", "sparse_attend",
@@ -27,6 +28,8 @@ __all__ = [
     "SPA_SCORE_LOWRANK", "SPA_SCORE_TAYLOR_BLOCK", "SPA_SCORE_MINMAX_BLOCK", "SPA_SCORE_MEAN_BLOCK",
     "SPA_SELECT_TOPK", "SPA_SELECT_TOPP", "SPA_STATS_BF16", "block_minmax", "rla_state",
     "SPA_DECODE_AUTO", "SPA_DECODE_SEPARATE", "SPA_DECODE_FUSED", "pbs_prefill", "PbsPlan",
+    "SPA_KV_BF16", "SPA_KV_INT4", "paged_cache", "paged_append", "PagedAppendPlan", "paged_gather", "PagedGatherPlan",
+    "paged_attend", "PagedAttendPlan",
 ]
 
 
@@ -427,6 +430,260 @@ def pbs_prefill(*, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, sm_scale: 
     a.out, a.out_f32 = _ptr(out), _ptr(out32)
     ws = workspace(lib().spa_pbs_workspace_bytes(ctypes.byref(a)), dev)
     plan = PbsPlan(a, ws, imp, perm, idx, count, out, out32, (Q, K, V))
+    if run:
+        plan.run()
+    return plan
+
+
+# ----------------------------------------------------------------------------- paged KV cache
+def paged_cache(num_pages: int, Hkv: int, page: int, d: int, fmt: int = SPA_KV_INT4, device=None) -> torch.Tensor:
+    """A zero-filled pool of pages: uint8 [num_pages, Hkv, page, d + 16] (SPA_KV_INT4) or bf16
+    [num_pages, Hkv, page, 2, d] (SPA_KV_BF16); see the paged KV cache in include/spa.h."""
+    if fmt == SPA_KV_BF16:
+        return torch.zeros((num_pages, Hkv, page, 2, d), dtype=torch.bfloat16, device=device or "cuda")
+    if fmt != SPA_KV_INT4:
+        raise ValueError(f"unknown cache format {fmt}")
+    row = lib().spa_paged_row_bytes(fmt, d)
+    return torch.zeros((num_pages, Hkv, page, row), dtype=torch.uint8, device=device or "cuda")
+
+
+def _same_device(ref: torch.Tensor, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {ref.device}")
+
+
+def _paged_kv(cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor) -> SpaPagedKv:
+    if cache.dtype == torch.bfloat16 and cache.dim() == 5 and cache.shape[3] == 2:
+        fmt, d = SPA_KV_BF16, cache.shape[4]
+    elif cache.dtype == torch.uint8 and cache.dim() == 4:
+        fmt, d = SPA_KV_INT4, cache.shape[3] - 16
+    else:
+        raise TypeError("cache must be bf16 [pages, Hkv, page, 2, d] or uint8 [pages, Hkv, page, d + 16]")
+    _need(cache, cache.dtype, "cache")
+    _need(page_table, torch.int32, "page_table")
+    _need(kv_len, torch.int32, "kv_len")
+    if page_table.dim() != 2 or tuple(kv_len.shape) != (page_table.shape[0],):
+        raise ValueError("page_table must be [B, max_pages] and kv_len [B]")
+    _same_device(cache, page_table=page_table, kv_len=kv_len)
+    kv = SpaPagedKv()
+    kv.format, kv.d = fmt, d
+    kv.num_pages, kv.Hkv, kv.page = cache.shape[0], cache.shape[1], cache.shape[2]
+    kv.B, kv.max_pages = page_table.shape
+    kv.data, kv.page_table, kv.kv_len = _ptr(cache), _ptr(page_table), _ptr(kv_len)
+    return kv
+
+
+def _rows(t: torch.Tensor, name: str, heads: Optional[int], d: int, T: Optional[int] = None) -> None:
+    """bf16 [T, heads, d] on a CUDA device, channels contiguous; token and head strides are free."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads) or (
+            T is not None and t.shape[0] != T):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [{'T' if T is None else T}, "
+                         f"{'heads' if heads is None else heads}, {d}]")
+    if t.numel() and t.stride(2) != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+
+
+def _seq_start(seq_start: Optional[torch.Tensor], T: int, kv: SpaPagedKv) -> None:
+    if seq_start is None:
+        if T != kv.B:
+            raise ValueError(f"without seq_start there is one new token per sequence: got {T} for {kv.B} sequences")
+        return
+    _need(seq_start, torch.int32, "seq_start")
+    if tuple(seq_start.shape) != (kv.B + 1,):
+        raise ValueError(f"seq_start must be [{kv.B + 1}], got {tuple(seq_start.shape)}")
+
+
+class _PagedPlan:
+    """run() of the paged plans."""
+
+    def run(self, stream: Optional[torch.cuda.Stream] = None) -> None:
+        """Launches the call on `stream` (default: the current stream of the cache's device).  kv_len,
+        page_table and the other tensors are read as they are when the kernels run.  Calls that share a
+        workspace must not overlap on the GPU: one plan on two streams at once is such a pair."""
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if s.device != self.device:
+            raise ValueError(f"stream is on {s.device}, the cache on {self.device}")
+        if s.cuda_stream not in self._streams:
+            self._meet(s)
+        if torch.cuda.current_device() == self.device.index:
+            check(self._fn(ctypes.byref(self.args), self.ws.data_ptr(), self.ws.numel(),
+                           ctypes.c_void_p(s.cuda_stream)), self._what)
+            return
+        with torch.cuda.device(self.device):
+            check(self._fn(ctypes.byref(self.args), self.ws.data_ptr(), self.ws.numel(),
+                           ctypes.c_void_p(s.cuda_stream)), self._what)
+
+    def _meet(self, s: torch.cuda.Stream) -> None:
+        # A stream other than the one the plan was built on: what that one still has to do to the plan's own
+        # tensors (the workspace's zero fill) comes first, and the allocator learns of the new stream.  A
+        # capture cannot wait for work outside it: there the graph's own rules hold.
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                return
+        s.wait_event(self._built)
+        for t in (self.ws, *self._own, *self.keep):
+            if t is not None:
+                t.record_stream(s)
+        self._streams.add(s.cuda_stream)
+
+    def _start(self, cache: torch.Tensor, what: str, ws: Optional[torch.Tensor], nbytes: int, own: tuple) -> None:
+        self.device, self._what, self._fn, self._own = cache.device, what, getattr(lib(), what), own
+        if ws is not None:
+            _need(ws, torch.uint8, "ws")
+            _same_device(cache, ws=ws)
+        self.ws = workspace(nbytes, cache.device) if ws is None else ws
+        here = torch.cuda.current_stream(self.device)
+        self._streams = {here.cuda_stream}
+        self._built = torch.cuda.Event()
+        with torch.cuda.stream(here):
+            if not torch.cuda.is_current_stream_capturing():
+                self._built.record(here)
+
+
+class PagedAppendPlan(_PagedPlan):
+    """Arguments, output and workspace (its status word) of one append, built once and reused."""
+
+    def __init__(self, args: SpaPagedAppendArgs, q_out: Optional[torch.Tensor], keep: tuple):
+        self.args, self.q_out, self.keep = args, q_out, keep
+
+
+def paged_append(*, k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor,
+                 kv_len: torch.Tensor, seq_start: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, inv_freq: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, interleaved: bool = False,
+                 ws: Optional[torch.Tensor] = None, run: bool = True) -> PagedAppendPlan:
+    """Append new tokens to a paged cache, rotating keys (and queries) on the way; see spa_paged_append in
+    include/spa.h.  k, v [T, Hkv, d] and q [T, Hq, d] bf16 (slices of a fused projection need no copy), cache
+    from paged_cache(), page_table [B, max_pages], kv_len [B] (the new tokens included), seq_start [B + 1] and
+    positions [T] int32; inv_freq [rot / 2] fp32 (None: no rotation).  The rotated queries are plan.q_out."""
+    kv = _paged_kv(cache, page_table, kv_len)
+    _rows(k, "k", kv.Hkv, kv.d)
+    T = k.shape[0]
+    _rows(v, "v", kv.Hkv, kv.d, T)
+    _seq_start(seq_start, T, kv)
+    a = SpaPagedAppendArgs()
+    a.kv, a.T = kv, T
+    if q is not None:
+        _rows(q, "q", None, kv.d, T)
+        if q_out is None:
+            q_out = torch.empty(tuple(q.shape), dtype=torch.bfloat16, device=q.device)
+        _need(q_out, torch.bfloat16, "q_out")
+        if tuple(q_out.shape) != tuple(q.shape):
+            raise ValueError(f"q_out must have shape {tuple(q.shape)}, got {tuple(q_out.shape)}")
+        a.Hq, a.q, a.q_out = q.shape[1], _ptr(q), _ptr(q_out)
+        a.q_token_stride, a.q_head_stride = q.stride(0), q.stride(1)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    a.k, a.k_token_stride, a.k_head_stride = _ptr(k), k.stride(0), k.stride(1)
+    a.v, a.v_token_stride, a.v_head_stride = _ptr(v), v.stride(0), v.stride(1)
+    a.seq_start, a.positions = _ptr(seq_start), _ptr(positions)
+    if positions is not None:
+        _need(positions, torch.int32, "positions")
+        if tuple(positions.shape) != (T,):
+            raise ValueError(f"positions must be [{T}], got {tuple(positions.shape)}")
+    if inv_freq is not None:
+        _need(inv_freq, torch.float32, "inv_freq")
+        if inv_freq.dim() != 1 or 2 * inv_freq.numel() > kv.d:
+            raise ValueError(f"inv_freq must be [rot / 2] with rot <= {kv.d}, got {tuple(inv_freq.shape)}")
+        a.inv_freq, a.rot = _ptr(inv_freq), 2 * inv_freq.numel()
+    a.interleaved = int(interleaved)
+    _same_device(cache, k=k, v=v, q=q, q_out=q_out, seq_start=seq_start, positions=positions, inv_freq=inv_freq)
+    plan = PagedAppendPlan(a, q_out, (k, v, q, cache, page_table, kv_len, seq_start, positions, inv_freq))
+    plan._start(cache, "spa_paged_append", ws, 256, (q_out,))
+    if run:
+        plan.run()
+    return plan
+
+
+class PagedGatherPlan(_PagedPlan):
+    """Arguments, outputs and workspace (its status word) of one gather, built once and reused."""
+
+    def __init__(self, args: SpaPagedGatherArgs, K: torch.Tensor, V: torch.Tensor, keep: tuple):
+        self.args, self.K, self.V, self.keep = args, K, V, keep
+
+
+def paged_gather(*, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor, N: int,
+                 start: Optional[torch.Tensor] = None, K: Optional[torch.Tensor] = None,
+                 V: Optional[torch.Tensor] = None, ws: Optional[torch.Tensor] = None,
+                 run: bool = True) -> PagedGatherPlan:
+    """Read tokens start[b] .. start[b] + N - 1 of every sequence back as dense bf16 plan.K, plan.V
+    [B, Hkv, N, d], the layout of decode(), prefill() and rla_state(); rows at and past kv_len[b] stay as they
+    are (zero in tensors allocated here).  See spa_paged_gather in include/spa.h."""
+    kv = _paged_kv(cache, page_table, kv_len)
+    shape = (kv.B, kv.Hkv, int(N), kv.d)
+    if N < 0:
+        raise ValueError("N must not be negative")
+    K = torch.zeros(shape, dtype=torch.bfloat16, device=cache.device) if K is None else K
+    V = torch.zeros(shape, dtype=torch.bfloat16, device=cache.device) if V is None else V
+    for t, n in ((K, "K"), (V, "V")):
+        _need(t, torch.bfloat16, n)
+        if tuple(t.shape) != shape:
+            raise ValueError(f"{n} must have shape {shape}, got {tuple(t.shape)}")
+    if start is not None:
+        _need(start, torch.int32, "start")
+        if tuple(start.shape) != (kv.B,):
+            raise ValueError(f"start must be [{kv.B}], got {tuple(start.shape)}")
+    _same_device(cache, K=K, V=V, start=start)
+    a = SpaPagedGatherArgs()
+    a.kv, a.N, a.start, a.K, a.V = kv, int(N), _ptr(start), _ptr(K), _ptr(V)
+    plan = PagedGatherPlan(a, K, V, (cache, page_table, kv_len, start))
+    plan._start(cache, "spa_paged_gather", ws, 256, (K, V))
+    if run:
+        plan.run()
+    return plan
+
+
+class PagedAttendPlan(_PagedPlan):
+    """Arguments, outputs and workspace of one attention call over a paged cache, built once and reused."""
+
+    def __init__(self, args: SpaPagedAttendArgs, out: torch.Tensor, out_f32: Optional[torch.Tensor],
+                 lse: Optional[torch.Tensor], keep: tuple):
+        self.args, self.out, self.out_f32, self.lse, self.keep = args, out, out_f32, lse, keep
+
+
+def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_len: torch.Tensor,
+                 sm_scale: float, seq_start: Optional[torch.Tensor] = None, idx: Optional[torch.Tensor] = None,
+                 count: Optional[torch.Tensor] = None, collapse: int = SPA_COLLAPSE_GROUP_MEAN, unit_tokens: int = 1,
+                 want_f32: bool = False, want_lse: bool = True, ws: Optional[torch.Tensor] = None,
+                 run: bool = True) -> PagedAttendPlan:
+    """Exact softmax attention of the new tokens over a paged cache (bf16 or 4-bit); see spa_paged_attend in
+    include/spa.h.  q [T, Hq, d] bf16.  Whole cache: every query sees the tokens up to its own; seq_start
+    [B + 1] int32 groups several queries per sequence.  Supports: idx [U, cap], count [U] int32 as select_topk
+    and select_topp give them, one query per sequence.  plan.out [T, Hq, d] bf16, plan.out_f32, plan.lse [T, Hq]."""
+    kv = _paged_kv(cache, page_table, kv_len)
+    _rows(q, "q", None, kv.d)
+    T, Hq, d = q.shape
+    _seq_start(seq_start, T, kv)
+    if (idx is None) != (count is None):
+        raise ValueError("idx and count go together")
+    a = SpaPagedAttendArgs()
+    a.kv, a.T, a.Hq, a.sm_scale = kv, T, Hq, sm_scale
+    a.seq_start, a.q, a.q_token_stride, a.q_head_stride = _ptr(seq_start), _ptr(q), q.stride(0), q.stride(1)
+    a.collapse, a.unit_tokens = collapse, unit_tokens
+    if idx is not None:
+        if seq_start is not None:
+            raise ValueError("supports take one query per sequence, without seq_start")
+        U = kv.B * (kv.Hkv if collapse == SPA_COLLAPSE_GROUP_MEAN else Hq)
+        _need(idx, torch.int32, "idx")
+        _need(count, torch.int32, "count")
+        if idx.dim() != 2 or idx.shape[0] != U or tuple(count.shape) != (U,):
+            raise ValueError(f"idx must be [{U}, cap] and count [{U}]")
+        a.idx, a.count, a.cap = _ptr(idx), _ptr(count), idx.shape[1]
+    _same_device(cache, q=q, seq_start=seq_start, idx=idx, count=count)
+    dev = cache.device
+    out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    out32 = torch.empty((T, Hq, d), dtype=torch.float32, device=dev) if want_f32 else None
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    a.out, a.out_f32, a.lse = _ptr(out), _ptr(out32), _ptr(lse)
+    plan = PagedAttendPlan(a, out, out32, lse, (q, cache, page_table, kv_len, seq_start, idx, count))
+    with torch.cuda.device(dev):
+        plan._start(cache, "spa_paged_attend", ws, lib().spa_paged_attend_workspace_bytes(d),
+                    (out, out32, lse))
     if run:
         plan.run()
     return plan

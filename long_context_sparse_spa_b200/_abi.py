@@ -32,11 +32,14 @@ SPA_TEST_STALL_PREFILL_MMA = 2
 SPA_DECODE_AUTO = 0
 SPA_DECODE_SEPARATE = 1
 SPA_DECODE_FUSED = 2
+SPA_KV_BF16 = 0
+SPA_KV_INT4 = 1
 
 _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_i64 = ctypes.c_int64
 
 
 class SpaDecodeArgs(ctypes.Structure):
@@ -81,6 +84,36 @@ class SpaPbsArgs(ctypes.Structure):
     ]
 
 
+class SpaPagedKv(ctypes.Structure):
+    _fields_ = [
+        ("format", _i), ("num_pages", _i), ("Hkv", _i), ("page", _i), ("d", _i), ("B", _i), ("max_pages", _i),
+        ("data", _p), ("page_table", _p), ("kv_len", _p),
+    ]
+
+
+class SpaPagedAppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("kv", SpaPagedKv), ("T", _i), ("Hq", _i), ("seq_start", _p), ("positions", _p),
+        ("k", _p), ("v", _p), ("q", _p),
+        ("k_token_stride", _i64), ("k_head_stride", _i64), ("v_token_stride", _i64), ("v_head_stride", _i64),
+        ("q_token_stride", _i64), ("q_head_stride", _i64),
+        ("q_out", _p), ("inv_freq", _p), ("rot", _i), ("interleaved", _i),
+    ]
+
+
+class SpaPagedGatherArgs(ctypes.Structure):
+    _fields_ = [("kv", SpaPagedKv), ("N", _i), ("start", _p), ("K", _p), ("V", _p)]
+
+
+class SpaPagedAttendArgs(ctypes.Structure):
+    _fields_ = [
+        ("kv", SpaPagedKv), ("T", _i), ("Hq", _i), ("seq_start", _p),
+        ("q", _p), ("q_token_stride", _i64), ("q_head_stride", _i64),
+        ("idx", _p), ("count", _p), ("cap", _i), ("collapse", _i), ("unit_tokens", _i), ("sm_scale", _f),
+        ("out", _p), ("out_f32", _p), ("lse", _p),
+    ]
+
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "spa_status_string": (ctypes.c_char_p, [_i]),
@@ -113,6 +146,11 @@ SIGNATURES = {
     "spa_pbs_prefill_timed": (_i, [ctypes.POINTER(SpaPbsArgs), _p, _sz, _p, ctypes.POINTER(_p)]),
     "spa_pbs_workspace_bytes": (_sz, [ctypes.POINTER(SpaPbsArgs)]),
     "spa_prefill_per_query_workspace_bytes": (_sz, [ctypes.POINTER(SpaPrefillArgs)]),
+    "spa_paged_row_bytes": (_sz, [_i, _i]),
+    "spa_paged_append": (_i, [ctypes.POINTER(SpaPagedAppendArgs), _p, _sz, _p]),
+    "spa_paged_gather": (_i, [ctypes.POINTER(SpaPagedGatherArgs), _p, _sz, _p]),
+    "spa_paged_attend": (_i, [ctypes.POINTER(SpaPagedAttendArgs), _p, _sz, _p]),
+    "spa_paged_attend_workspace_bytes": (_sz, [_i]),
 }
 
 _LIB = None

@@ -1,0 +1,282 @@
+// Paged KV cache: appending new keys and values with the position rotation on the way, in bf16 or
+// quantised to 4 bits, and reading rows back as dense bf16.  The method pages have no counterpart;
+// the cache feeds the same attention and selection as the dense [B, Hkv, N, d] one.
+//
+// Append, per new token t of sequence b at position n (its slot in the cache):
+//   the rotation turns channel pairs (x, y) of q and k by the angle a_i = pos * inv_freq[i]:
+//     x' = x cos a_i - y sin a_i,  y' = y cos a_i + x sin a_i;
+//   a bf16 cache takes k' and v rounded once; a 4-bit cache takes, per group of d/4 channels,
+//     s = amax / 7 rounded up to bf16,  code = rint(x / s) + 8, x / s in [-7, 7].
+//   Rounding the scale up keeps every quotient within [-7, 7], so no code clamps and the error of a
+//   value is at most s/2.  Codes are taken from the rotated keys in fp32, not from their bf16 rounding.
+//   A group that holds a NaN or an infinity gets the scale NaN: it reads back as NaN, never as a number.
+// Angles and their sine and cosine are computed in fp64 (a position of 10^6 leaves fp32 only 0.06 rad),
+// the rotation itself in fp32 without contraction.
+//
+// Each row of d channels is held by d/8 lanes, 8 channels (16 bytes) each; pair partners and group
+// maxima are exchanged by shuffles, so a row is read once and nothing is written before it is read.
+#include "paged.cuh"
+
+namespace spa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAppTok = 4;   // tokens per CTA: 4 x 64 angles are one per thread at d = 128
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// ------------------------------------------------------------------ append
+template <int D, bool INT4>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParams p, int tok_per_cta) {
+    constexpr int LPR = D / 8;              // lanes per row
+    constexpr int RPP = kThreads / LPR;     // rows per pass
+    constexpr int GL = LPR / 4;             // lanes per quantisation group
+    __shared__ float s_cos[kAppTok][64], s_sin[kAppTok][64];
+    __shared__ long long s_row[kAppTok];    // byte offset of the token's row of kv head 0, or -1
+    __shared__ int s_pos[kAppTok];
+    __shared__ __align__(16) uint8_t s_val[INT4 ? RPP : 1][INT4 ? D / 2 : 16];
+    pdl_enter();
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * tok_per_cta;
+    const int nt = min(tok_per_cta, p.T - t0);
+    if (tid < nt) {
+        const int t = t0 + tid;
+        long long row = -1;
+        int rope = 0;
+        const int b = paged_seq_of(p.seq_start, p.kv.B, t);
+        if (b >= 0) {
+            // slot of the token: the last of the sequence's new tokens is token kv_len[b] - 1
+            const long long left = p.seq_start ? (long long)p.seq_start[b + 1] - t : 1;
+            const long long n = (long long)p.kv.kv_len[b] - left;
+            const long long slot = paged_slot(p.kv, b, n);
+            if (slot >= 0) row = paged_row(p.kv, p.kv.page_table[slot], 0, n);
+            if (row < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+            rope = p.positions ? p.positions[t] : int(n);
+        }
+        s_row[tid] = row;
+        s_pos[tid] = rope;
+    }
+    __syncthreads();
+    const int half = p.rot / 2;
+    for (int i = tid; i < nt * half; i += kThreads) {
+        const int t = i / half, f = i - t * half;
+        if (s_row[t] < 0) continue;
+        double sn, cs;
+        sincos(double(s_pos[t]) * double(p.inv_freq[f]), &sn, &cs);
+        s_cos[t][f] = float(cs);
+        s_sin[t][f] = float(sn);
+    }
+    __syncthreads();
+
+    const int Hkv = p.kv.Hkv, Hq = p.q ? p.Hq : 0;
+    const int rows = Hq + 2 * Hkv;          // rows of a token: queries, keys, values
+    const int c = tid % LPR;                // this lane's 8 channels: [8c, 8c + 8)
+    const int total = nt * rows;
+    const long long head_bytes = (long long)p.kv.row_bytes << p.kv.page_shift;
+    for (int base = 0; base < total; base += RPP) {   // same trip count for every lane: shuffles below
+        const int ri = base + tid / LPR;
+        const int t = min(ri / rows, nt - 1), r = ri - t * rows;
+        const bool live = ri < total && s_row[t] >= 0;
+        const int kind = r < Hq ? 0 : r < Hq + Hkv ? 1 : 2;   // query, key, value
+        const int h = kind == 0 ? r : kind == 1 ? r - Hq : r - Hq - Hkv;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (live) {
+            const uint16_t* src = kind == 0   ? p.q + (t0 + t) * p.q_tok + h * p.q_head
+                                  : kind == 1 ? p.k + (t0 + t) * p.k_tok + h * p.k_head
+                                              : p.v + (t0 + t) * p.v_tok + h * p.v_head;
+            w = __ldg(reinterpret_cast<const uint4*>(src) + c);
+        }
+        float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y), bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
+        if (p.interleaved) {
+            if (kind < 2 && 8 * c < p.rot) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float cs = s_cos[t][4 * c + j], sn = s_sin[t][4 * c + j];
+                    const float a = x[2 * j], b = x[2 * j + 1];
+                    x[2 * j] = __fsub_rn(__fmul_rn(a, cs), __fmul_rn(b, sn));
+                    x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs), __fmul_rn(a, sn));
+                }
+            }
+        } else if (p.rot > 0) {
+            const int hc = p.rot / 16;      // lanes per half of the rotated channels
+            const bool turn = c < 2 * hc;
+            const int mate = !turn ? c : c < hc ? c + hc : c - hc;
+            const int src = (threadIdx.x & 31) - c % 32 + mate;   // the partner lane of the same row
+            uint4 o;
+            o.x = __shfl_sync(0xffffffffu, w.x, src);
+            o.y = __shfl_sync(0xffffffffu, w.y, src);
+            o.z = __shfl_sync(0xffffffffu, w.z, src);
+            o.w = __shfl_sync(0xffffffffu, w.w, src);
+            if (kind < 2 && turn) {
+                const float y[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
+                                    bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
+                const int f0 = (c < hc ? c : c - hc) * 8;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float cs = s_cos[t][f0 + j], sn = s_sin[t][f0 + j];
+                    x[j] = c < hc ? __fsub_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn))
+                                  : __fadd_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn));
+                }
+            }
+        }
+        if (kind == 0 || !INT4) {
+            if (live) {
+                const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                                           pack_bf16(x[6], x[7]));
+                uint8_t* dst = kind == 0 ? reinterpret_cast<uint8_t*>(p.q_out + (size_t(t0 + t) * p.Hq + h) * D)
+                                         : p.kv.data + s_row[t] + h * head_bytes + (kind == 2 ? 2 * D : 0);
+                reinterpret_cast<uint4*>(dst)[c] = o;
+            }
+        }
+        if constexpr (INT4) {
+            // group maximum; an element that is not finite poisons the group
+            float top = 0.f;
+            bool bad = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                bad |= !(fabsf(x[j]) <= 3.402823466e38f);
+                top = fmaxf(top, fabsf(x[j]));
+            }
+            if (bad) top = __uint_as_float(0x7f800000u);
+#pragma unroll
+            for (int off = 1; off < GL; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            // up to bf16: the scale must not be below amax / 7, so that no code clamps
+            const bool fin = top <= 3.402823466e38f;
+            const uint32_t sb = fin ? (__float_as_uint(__fdiv_rn(top, 7.f)) + 0xffffu) & 0xffff0000u : 0x7fc00000u;
+            const float s = __uint_as_float(sb);
+            uint32_t nib = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int code = fin && s > 0.f ? __float2int_rn(__fdiv_rn(x[j], s)) : 0;
+                nib |= uint32_t(code + 8) << (4 * j);
+            }
+            uint8_t* dst = p.kv.data + (live ? s_row[t] + h * head_bytes : 0);
+            const int g = c / GL;
+            if (live && kind > 0 && c % GL == 0)
+                reinterpret_cast<uint16_t*>(dst + D)[(kind == 2 ? 4 : 0) + g] = uint16_t(sb >> 16);
+            if (kind == 1 && live) {
+                if constexpr (D == 128) {   // a lane's 8 channels are one lane-of-a-quad's share of its group
+                    *reinterpret_cast<uint32_t*>(dst + (c % 4) * 16 + g * 4) = nib;
+                } else {
+                    *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + g * 2) = uint16_t(nib);
+                    *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + 8 + g * 2) = uint16_t(nib >> 16);
+                }
+            }
+            // values: channels 16 i + r and 16 i + r + 8 share byte r * D/16 + (c / 2), so an even lane joins its
+            // neighbour's codes to its own; the row's bytes go through shared memory and out in 16-byte stores
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, nib, 1);
+            uint8_t* sv = s_val[tid / LPR];
+            __syncwarp();
+            if (c % 2 == 0) {
+#pragma unroll
+                for (int r8 = 0; r8 < 8; ++r8)
+                    sv[r8 * (D / 16) + c / 2] = uint8_t(((nib >> (4 * r8)) & 15u) | (((other >> (4 * r8)) & 15u) << 4));
+            }
+            __syncwarp();
+            if (kind == 2 && live && c < D / 32)
+                *reinterpret_cast<uint4*>(dst + D / 2 + 16 * c) = *reinterpret_cast<const uint4*>(sv + 16 * c);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ gather
+// One CTA per 64 tokens of one (sequence, kv head): the rows' bytes are staged in shared memory with
+// 16-byte loads and written as 16-byte pieces of the dense rows.
+constexpr int kGatTok = 64;
+
+template <int D, bool INT4>
+__global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherParams p) {
+    constexpr int ROWB = INT4 ? D + 16 : 4 * D;
+    constexpr int LPR = D / 8;
+    __shared__ long long s_row[kGatTok];
+    __shared__ __align__(16) uint8_t s_in[INT4 ? kGatTok * ROWB : 16];
+    pdl_enter();
+    const int tid = threadIdx.x;
+    const int g = blockIdx.y, b = blockIdx.z;
+    const long long i0 = (long long)blockIdx.x * kGatTok;
+    bool bad = false;
+    const int len = paged_len(p.kv, p.kv.kv_len[b], &bad);
+    const long long first = p.start ? p.start[b] : 0;
+    if (tid < kGatTok) {
+        long long row = -1;
+        const long long i = i0 + tid, n = first + i;
+        if (i < p.N && n >= 0 && n < len) {
+            row = paged_row(p.kv, p.kv.page_table[paged_slot(p.kv, b, n)], g, n);
+            bad |= row < 0;
+        }
+        s_row[tid] = row;
+        if (bad || first < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+    }
+    __syncthreads();
+    uint16_t* const outs[2] = {p.K, p.V};
+    if constexpr (INT4) {
+        constexpr int CH = ROWB / 16;
+        for (int i = tid; i < kGatTok * CH; i += kThreads) {
+            const int t = i / CH, ch = i - t * CH;
+            if (s_row[t] >= 0)
+                reinterpret_cast<uint4*>(s_in)[i] = __ldg(reinterpret_cast<const uint4*>(p.kv.data + s_row[t]) + ch);
+        }
+        __syncthreads();
+    }
+    for (int i = tid; i < kGatTok * 2 * LPR; i += kThreads) {
+        const int t = i / (2 * LPR), r = i - t * 2 * LPR, isv = r / LPR, c = r - isv * LPR;
+        if (s_row[t] < 0) continue;
+        uint4 o;
+        if constexpr (INT4) {
+            const uint8_t* row = s_in + t * ROWB;
+            const int gr = c / (LPR / 4);
+            const float s = bf_lo(reinterpret_cast<const uint16_t*>(row + D)[isv * 4 + gr]);
+            uint32_t nib;
+            if (!isv) {
+                if constexpr (D == 128) nib = *reinterpret_cast<const uint32_t*>(row + (c % 4) * 16 + gr * 4);
+                else
+                    nib = *reinterpret_cast<const uint16_t*>(row + (c % 2) * 16 + gr * 2) |
+                          uint32_t(*reinterpret_cast<const uint16_t*>(row + (c % 2) * 16 + 8 + gr * 2)) << 16;
+            } else {
+                nib = 0;
+#pragma unroll
+                for (int r8 = 0; r8 < 8; ++r8)
+                    nib |= ((uint32_t(row[D / 2 + r8 * (D / 16) + c / 2]) >> (4 * (c & 1))) & 15u) << (4 * r8);
+            }
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = float(int((nib >> (4 * j)) & 15u) - 8) * s;
+            o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        } else {
+            o = __ldg(reinterpret_cast<const uint4*>(p.kv.data + s_row[t] + isv * 2 * D) + c);
+        }
+        reinterpret_cast<uint4*>(outs[isv] + ((size_t(b) * p.kv.Hkv + g) * p.N + i0 + t) * D)[c] = o;
+    }
+}
+
+}  // namespace
+
+spa_status launch_paged_append(const PagedAppendParams& p, cudaStream_t st) {
+    // tokens per CTA: as few as fill the SMs (a decode step has one token per sequence), at most kAppTok
+    const int sms = device_info().num_sms;
+    const int tok = p.T >= 4 * sms ? kAppTok : p.T >= 2 * sms ? 2 : 1;
+    const dim3 grid((p.T + tok - 1) / tok);
+#define SPA_APP(DD, I4)                                                                                   \
+    if (p.kv.d == DD && (p.kv.int4 != 0) == I4)                                                           \
+        SPA_CUDA_TRY(launch_pdl(paged_append_kernel<DD, I4>, grid, dim3(kThreads), 0, st, p, tok));
+    SPA_APP(64, false) SPA_APP(64, true) SPA_APP(128, false) SPA_APP(128, true)
+#undef SPA_APP
+    return SPA_OK;
+}
+
+spa_status launch_paged_gather(const PagedGatherParams& p, cudaStream_t st) {
+    const dim3 grid((p.N + kGatTok - 1) / kGatTok, p.kv.Hkv, p.kv.B);
+#define SPA_GAT(DD, I4)                                                                       \
+    if (p.kv.d == DD && (p.kv.int4 != 0) == I4)                                               \
+        SPA_CUDA_TRY(launch_pdl(paged_gather_kernel<DD, I4>, grid, dim3(kThreads), 0, st, p));
+    SPA_GAT(64, false) SPA_GAT(64, true) SPA_GAT(128, false) SPA_GAT(128, true)
+#undef SPA_GAT
+    return SPA_OK;
+}
+
+}  // namespace spa

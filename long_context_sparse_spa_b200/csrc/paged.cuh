@@ -1,0 +1,52 @@
+// Declarations shared by the paged KV cache kernels (paged.cu, paged_attend.cu) and their host side.
+#pragma once
+#include "internal.cuh"
+#include "paged_map.h"
+
+namespace spa {
+
+struct PagedAppendParams {
+    PagedView kv;
+    int T, Hq;
+    const int32_t* seq_start;   // [B + 1] or null
+    const int32_t* positions;   // [T] or null
+    const uint16_t *k, *v, *q;  // q null: keys and values only
+    long long k_tok, k_head, v_tok, v_head, q_tok, q_head;   // strides in elements
+    uint16_t* q_out;            // [T, Hq, d]
+    const float* inv_freq;      // [rot / 2]
+    int rot, interleaved;
+    uint32_t* status;
+};
+spa_status launch_paged_append(const PagedAppendParams& p, cudaStream_t st);
+
+struct PagedGatherParams {
+    PagedView kv;
+    int N;
+    const int32_t* start;       // [B] or null
+    uint16_t *K, *V;            // [B, Hkv, N, d]
+    uint32_t* status;
+};
+spa_status launch_paged_gather(const PagedGatherParams& p, cudaStream_t st);
+
+struct PagedAttendParams {
+    PagedView kv;
+    int T, Hq;
+    const int32_t* seq_start;
+    const uint16_t* q;
+    long long q_tok, q_head;
+    const int32_t* idx;         // null: every cached token
+    const int32_t* count;
+    int cap, collapse, unit_tokens;
+    float sm_scale;
+    uint16_t* out;              // [T, Hq, d]
+    float* out_f32;
+    float* lse;                 // [T, Hq]
+    int4* split;                // [grid]: unit split over CTAs [c, hi] that starts in CTA c
+    float* partials;            // [2 * grid][16][d + 2]
+    uint32_t* status;
+};
+spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
+size_t paged_attend_scratch_bytes(int d);
+constexpr int kPagedMaxUnits = 2048;   // sequences, or supports, of one launch: 8 bytes of shared memory each
+
+}  // namespace spa
