@@ -41,12 +41,13 @@ struct PagedAttendParams {
     uint16_t* out;              // [T, Hq, d]
     float* out_f32;
     float* lse;                 // [T, Hq]
-    int4* split;                // [grid]: unit split over CTAs [c, hi] that starts in CTA c
-    float* partials;            // [2 * grid][16][d + 2]
+    int* arrived;               // [CTAs]: finished shares of the split unit that starts in a CTA; 0 between calls
+    float* partials;            // [2 * CTAs][16][d + 2]
     uint32_t* status;
 };
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_attend_scratch_bytes(int d);
-constexpr int kPagedMaxUnits = 2048;   // sequences, or supports, of one launch: 8 bytes of shared memory each
+void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch);   // the workspace after its header
+constexpr int kPagedMaxUnits = 512;   // sequences, or supports, of one launch: 4 bytes of shared memory each
 
 }  // namespace spa

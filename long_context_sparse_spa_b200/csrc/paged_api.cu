@@ -154,9 +154,7 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     p.out_f32 = a->out_f32;
     p.lse = a->lse;
     p.status = reinterpret_cast<uint32_t*>(w);
-    p.split = reinterpret_cast<int4*>(w + kWsHeader);
-    p.partials = reinterpret_cast<float*>(w + kWsHeader +
-                                          align_up(size_t(device_info().num_sms) * sizeof(int4), 256));
+    paged_attend_carve(p, w + kWsHeader);
     return launch_paged_attend(p, static_cast<cudaStream_t>(stream));
 }
 

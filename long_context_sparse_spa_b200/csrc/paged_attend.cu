@@ -13,29 +13,33 @@
 //     A nibble masked out of its word is an fp16 denormal, u * 2^-24 in bits 0-3 and u * 2^-20 in bits
 //     4-7: one AND per two codes makes the A operand, exactly.  q is scaled by a power of two into
 //     fp16's range (and by 1/16 for the second kind), exactly above 2^-24 of its largest channel; the
-//     -8 is the accumulator's start value, and the group scale multiplies in fp32.
-//   4-bit values: O += V^T W^T with W = p * s_g in fp16 (11 bits), V = u - 8 centred exactly in fp16.
-//     So that W fits fp16 whatever the scales are, the running reference of the softmax is the maximum
-//     of (logit + log2 of the token's largest value scale), not of the logit; p and l are relative to it
-//     in fp32, and W <= 2^15.
+//     group scale multiplies in fp32, and the -8 terms are one more product, scales times three bf16
+//     terms of the sums.
+//   4-bit values: with r_g = s_g / (the token's largest s) and P = p * (that largest s), both in fp16 (11
+//     bits), O += V^T P^T with V = (u - 8) r_g, one fp16 FMA per two codes after the AND.  A transposing
+//     ldmatrix over 16-bit units (four codes of a token) pairs tokens for the A operand.  So that P fits
+//     fp16 whatever the scales are, the running reference of the softmax is the maximum of (logit + log2 of
+//     the token's largest value scale), not of the logit; P <= 2^15, and l = sum p is kept in fp32.
 //   bf16 rows: S = K Q^T, O += V^T P^T with P = hi + lo bf16 (about 16 bits).
 // The m16 rows of a tile are a permutation of its tokens (tau) that keeps the shared-memory reads free
 // of bank conflicts for the rows' strides; a softmax does not see the order.
 //
 // At the end of its share of a unit a CTA merges its warps in shared memory and writes the output, or a
-// partial (o, m, l) if the unit is split; a second kernel merges partials in a fixed order.
+// partial (o, m, l) if the unit is split; the last CTA of a split unit to finish merges its partials in the
+// order of the CTAs, so equal calls give equal bits.
 #include "paged.cuh"
 #include "warp_mma.cuh"
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace spa {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRowsMax = 16;              // (query, head) rows of a unit
 constexpr int kSeg = 8;                   // tiles charged to a unit for its start-up and merge
+constexpr int kShare = 16;                // least weighted tiles of a CTA's share
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloorV = 8.077935669463161e-28f;   // 2^-90: least value scale that the reference follows
@@ -43,18 +47,21 @@ constexpr float kBase = 9.f;              // weights are 2^9 at the reference, a
 constexpr float kSlack = 6.f;             // the reference moves only when it is exceeded by this (log2)
 constexpr uint32_t kWaitLimit = 1u << 22;
 
-template <int D, bool INT4>
+template <int D, bool INT4, int NT>
 struct Geo {
     static constexpr int ROWB = INT4 ? D + 16 : 4 * D;
     static constexpr int TILE = INT4 ? 32 : 16;           // tokens per warp step
     static constexpr int MT = TILE / 16;
-    static constexpr int STAGES = INT4 ? 4 : 3;
+    static constexpr int STAGES = 3;
+    static constexpr int WARPS = 8;
+    static constexpr int CTAS = INT4 && NT == 1 ? 2 : 1;  // per SM
     // shared-memory row stride: bf16 rows are copied one by one and padded (a multiple of 128 bytes would put
     // the eight rows of a fragment on the same banks)
     static constexpr int SROW = INT4 ? ROWB : ROWB + 16;
-    static constexpr int RING = kWarps * STAGES * TILE * SROW;
-    static constexpr int MERGE = kWarps * kRowsMax * (D + 2) * 4;
-    static constexpr int SMEM = RING > MERGE ? RING : MERGE;
+    static constexpr int RING = WARPS * STAGES * TILE * SROW;
+    static constexpr int MERGE = WARPS * NT * 8 * (D + 2) * 4;
+    static constexpr int PREP = INT4 ? WARPS * TILE * 8 : 0;   // (log2, 1 / value) of each token's largest value scale
+    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + PREP;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -64,7 +71,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float lg2(float x) {
     float y;
-    asm("lg2.approx.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -73,18 +80,12 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                        const float (&c)[4]) {
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%10,%11,%12,%13};\n"
-        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+        "{%0,%1,%2,%3};\n"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
@@ -101,15 +102,40 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
     asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(v) : "r"(a));
     return v;
 }
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {   // of a number and a NaN the number
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};\n" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
 __device__ __forceinline__ void sts128_zero(uint32_t a) {
     asm volatile("st.shared.v4.u32 [%0], {%1,%1,%1,%1};\n" ::"r"(a), "r"(0) : "memory");
 }
 
-// Row r (0..7) of a 16-row tile is token tau(r), row r + 8 token tau(r) + 1 (4-bit) or tau(r) + 8 (bf16).
-// 4-bit: {0,4,2,6,12,8,14,10}; bf16: {0,4,1,5,2,6,3,7}.
-template <bool INT4>
+// Row r (0..7) of a 16-row tile is token tau(r), row r + 8 token tau(r) + 8.  Keys are read two (d = 128:
+// 16 bytes a lane) or four rows (d = 64) at a time, which must lie on different banks: rows of 144 and 528
+// bytes step by 4 banks, so d = 128 and bf16 want neighbours 4 apart, {0,4,1,5,2,6,3,7}; rows of 80 bytes step
+// by 20, so d = 64 wants {0,2,4,6,1,3,5,7}.  Transposing loads take any order of the eight.
+template <int D, bool INT4>
 __device__ __forceinline__ int tau(int r) {
-    return INT4 ? int((0xAE8C6240u >> (4 * r)) & 15u) : int((0x73625140u >> (4 * r)) & 15u);
+    return INT4 && D == 64 ? int((0x75316420u >> (4 * r)) & 15u) : int((0x73625140u >> (4 * r)) & 15u);
+}
+// the row that holds token n (0..7)
+template <int D, bool INT4>
+__device__ __forceinline__ int tau_inv(int n) {
+    return INT4 && D == 64 ? int((0x73625140u >> (4 * n)) & 15u) : int((0x75316420u >> (4 * n)) & 15u);
 }
 
 struct Unit {
@@ -158,17 +184,22 @@ __device__ __forceinline__ long long head_weight(const SeqGeo& s, int TQ) {
 }
 
 template <int D, bool INT4, int NT>
-__global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
-    using G_ = Geo<D, INT4>;
+__global__ void __launch_bounds__(Geo<D, INT4, NT>::WARPS * 32, Geo<D, INT4, NT>::CTAS)
+paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
+    using G_ = Geo<D, INT4, NT>;
+    constexpr int kWarps = G_::WARPS, kThreads = kWarps * 32, ROWS = NT * 8;
     constexpr int TILE = G_::TILE, ROWB = G_::ROWB, SROW = G_::SROW, STAGES = G_::STAGES, MT = G_::MT;
     constexpr int KS = D / 16;                 // k-steps of S, and 16-channel tiles of O
     constexpr int DT = D / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const ring = smem;
-    long long* const s_prefix = reinterpret_cast<long long*>(smem + G_::SMEM);   // [groups + 1]
+    uint32_t* const s_prefix = reinterpret_cast<uint32_t*>(smem + G_::SMEM);   // [groups + 1]
+    const uint32_t prep = smem_u32(smem + G_::SMEM - G_::PREP + (INT4 ? (threadIdx.x >> 5) * TILE * 8 : 0));
     __shared__ uint64_t s_full[kWarps][STAGES];
     __shared__ uint32_t s_vmask[kWarps][STAGES];
     __shared__ long long s_wsum[kWarps];
+    __shared__ int s_last;
+    __shared__ long long s_seg[3];       // the unit's first and last weighted tile, and where this CTA goes on
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int r8 = lane >> 2, t4 = lane & 3;
@@ -182,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
 
     // ---- weighted tile prefix over the groups [g0, g0 + groups): sequences (all kv heads), or supports
     long long running = 0;
+    bool empties = false;     // some query of the launch sees nothing
     for (int base = 0; base < groups; base += kThreads) {
         const int u = base + tid;
         long long t = 0;
@@ -189,10 +221,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             if (sparse) {
                 const int n = support_tokens(p, g0 + u);
                 t = n > 0 ? (n + TILE - 1) / TILE + kSeg : 0;
+                empties |= n == 0;
             } else {
                 bool bad = false;
                 const SeqGeo s = seq_geo(p, g0 + u, &bad);
                 t = head_weight<TILE>(s, TQ) * p.kv.Hkv;
+                empties |= s.n > 0 && paged_tile_limit(s.len, s.n, TQ, 0) == 0;
                 if (bad && blockIdx.x == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
             }
         }
@@ -210,15 +244,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             if (w < warp) before += s_wsum[w];
             tot += s_wsum[w];
         }
-        if (u < groups) s_prefix[u] = before + incl - t;
+        if (u < groups) s_prefix[u] = uint32_t(before + incl - t);
         running += tot;
         __syncthreads();
     }
-    if (tid == 0) s_prefix[groups] = running;
-    __syncthreads();
+    if (tid == 0) s_prefix[groups] = uint32_t(running);
+    empties = __syncthreads_or(empties);
     const long long TT = running;
     const int cta = blockIdx.x;
-    const int GC = int(TT < (long long)gridDim.x ? TT : (long long)gridDim.x);   // CTAs with work
+    // CTAs with work: none gets less than about kShare tiles, since every share of a unit is merged
+    const long long shares = (TT + kShare - 1) / kShare;
+    const int GC = int(shares < (long long)gridDim.x ? shares : (long long)gridDim.x);
 
     // ---- units without a key: out = 0, lse = -inf
     auto write_empty = [&](int row0, int nrow, int h0, int nh) {
@@ -230,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             if (p.lse && c == 0) p.lse[size_t(row0 + q) * p.Hq + h0 + h] = -INFINITY;
         }
     };
-    for (int u = cta; u < groups; u += gridDim.x) {
+    for (int u = cta; empties && u < groups; u += gridDim.x) {
         if (sparse) {
             if (s_prefix[u + 1] != s_prefix[u]) continue;
             const bool grp = p.collapse == SPA_COLLAPSE_GROUP_MEAN;
@@ -245,7 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                 write_empty(s.row0 + j * TQ, min(TQ, s.n - j * TQ), 0, p.Hq);
         }
     }
-    if (tid == 0) p.split[cta] = make_int4(-1, -1, -1, -1);
     if (cta >= GC) return;
 
     const long long x0 = TT * cta / GC, x1 = TT * (cta + 1) / GC;
@@ -259,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         grp = lo;
     }
     const float sl2 = p.sm_scale * kLog2e;
-    const int page = 1 << p.kv.page_shift;
     uint32_t phases = 0;      // parity of each stage's barrier
     bool failed = false;      // a wait gave up: the rest of this CTA's waits are short
     uint8_t* const my_ring = ring + size_t(warp) * STAGES * TILE * SROW;
@@ -319,17 +353,117 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
         const long long seg_end = x1 < u_hi ? x1 : u_hi;
         const int a = int(x - u_lo) - kSeg > 0 ? int(x - u_lo) - kSeg : 0;
         const int bnd = int(seg_end - u_lo) - kSeg > 0 ? int(seg_end - u_lo) - kSeg : 0;
-        const long long x_next = seg_end;
         if (a >= bnd) {       // only the unit's fixed cost lies in this CTA's range
-            x = x_next;
+            x = seg_end;
             continue;
+        }
+        if (tid == 0) {       // kept in shared memory over the tile loop
+            s_seg[0] = u_lo;
+            s_seg[1] = u_hi;
+            s_seg[2] = seg_end;
         }
         const int nrow = un.nq * un.heads;
 
+        // ---- copying: lane i fetches the i-th run of R tokens of a tile
+        const int ut = p.unit_tokens;
+        int rsh = !INT4 ? 0 : min(5, p.kv.page_shift);   // R = 1 << rsh
+        if (sparse) rsh = min(rsh, __ffs(ut) - 1);
+        const int R = 1 << rsh;
+        constexpr int kTileSh = TILE == 32 ? 5 : 4;
+        const int runsh = kTileSh - rsh;
+        const int n_my = a + warp < bnd ? (bnd - a - warp + kWarps - 1) / kWarps : 0;
+        const int persh = 5 - runsh;            // tiles whose runs the lanes hold at once (a batch): lane i has run
+        const int my_tile = lane >> runsh, my_run = lane & ((1 << runsh) - 1);   // my_run of the batch's tile my_tile
+        // first token of this lane's run in batch k of my tiles, or -1
+        auto token_of = [&](int k) -> int {
+            const int j = (k << persh) + my_tile;
+            if (j >= n_my) return -1;
+            const int i = (a + warp + j * kWarps) * TILE + my_run * R;
+            if (i >= un.ntok) return -1;
+            if (!sparse) return i;
+            const int e = ut == 1 ? i : i / ut;
+            const long long n = (long long)__ldg(p.idx + size_t(un.u) * p.cap + e) * ut + (i - e * ut);
+            return n >= 0 && n < un.len ? int(n) : -1;
+        };
+        auto page_of = [&](int n) -> int {
+            const long long s = paged_slot(p.kv, un.b, n);
+            return s < 0 ? -1 : __ldg(p.kv.page_table + s);
+        };
+        // the batch in hand: address and bytes of this lane's run
+        const uint8_t* src = nullptr;
+        int valid = 0;
+        auto take = [&](int n, int pid) {
+            valid = 0;                          // tokens of the run that exist
+            if (n < 0) return;
+            const long long off = paged_row(p.kv, pid, un.g, n);
+            if (off < 0) {
+                raise_status(p.status, SPA_ERR_INVALID_ARG);
+                return;
+            }
+            valid = min(R, un.len - n);
+            if (!sparse) valid = min(valid, un.ntok - n);
+            src = p.kv.data + off;
+        };
+        constexpr uint32_t kFull = TILE == 32 ? 0xffffffffu : (1u << TILE) - 1u;
+        int fill = 0;                           // the stage that is filled next
+        uint32_t ragged = 0;                    // runs of the batch in hand that are not whole
+        auto issue = [&](int j) {               // tile j of mine, which is in the batch in hand
+            const int stage = fill;
+            fill = fill + 1 == STAGES ? 0 : fill + 1;
+            const uint32_t bar = smem_u32(&s_full[warp][stage]);
+            const uint32_t dst = smem_u32(my_ring + size_t(stage) * TILE * SROW);
+            const int slot = j & ((1 << persh) - 1);
+            const bool mine = my_tile == slot;
+            uint32_t all = kFull;
+            if ((ragged >> (slot << runsh)) & ((2u << ((1 << runsh) - 1)) - 1u)) {
+                const uint32_t mask =
+                    mine && valid > 0 ? (valid >= 32 ? 0xffffffffu : ((1u << valid) - 1u)) << (my_run * R) : 0u;
+                all = __reduce_or_sync(0xffffffffu, mask);
+                // tokens that do not exist: nothing of them may reach an operand as NaN or infinity
+                if (mine)
+                    for (int i = valid; i < R; ++i) {
+                        const uint32_t row = dst + (my_run * R + i) * SROW;
+                        if (INT4) sts128_zero(row + D);
+                        else
+                            for (int c = 0; c < 4 * D; c += 16) sts128_zero(row + c);
+                    }
+                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
+            }
+            if (lane == 0) {
+                s_vmask[warp][stage] = all;
+                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar),
+                             "r"(uint32_t(__popc(all) * ROWB))
+                             : "memory");
+            }
+            __syncwarp();
+            if (mine && valid > 0)
+                asm volatile(
+                    "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+                        dst + my_run * R * SROW),
+                    "l"(src), "r"(uint32_t(valid * ROWB)), "r"(bar)
+                    : "memory");
+        };
+
+        // tokens are looked up two batches ahead of their copies and pages one ahead
+        int n1 = token_of(0), pg1 = page_of(n1), n2 = token_of(1);
+        int issued = 0;
+        auto advance = [&]() {                  // the next tile, if any, on its way
+            if (issued >= n_my) return;
+            if ((issued & ((1 << persh) - 1)) == 0) {
+                take(n1, pg1);
+                ragged = __ballot_sync(0xffffffffu, valid != R);
+                n1 = n2;
+                pg1 = page_of(n1);
+                n2 = token_of((issued >> persh) + 2);
+            }
+            issue(issued++);
+        };
+#pragma unroll 1
+        for (int j = 0; j < STAGES - 1; ++j) advance();
         // ---- queries as the B operand of S (column n = r8 of column tile nt), zero beyond nrow
         uint32_t qb[KS][NT][2];
         float hs[NT][2];                        // logit scale (log2 units) of this lane's two columns
-        float q0[INT4 ? 4 : 1][NT][2];          // 4-bit: start values -8 sum q of each group
+        uint32_t qz[NT][2];                     // 4-bit: -8 sum q of each group in three bf16 terms, as a B operand
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = nt * 8 + r8;
@@ -339,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             if constexpr (INT4) {
                 // lane t4's channels: D/16 consecutive ones of each of the 4 groups
                 constexpr int E = D / 16;
-                float f[4][E];
+                float f[4][E], z[4];
                 float top = 0.f;
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
@@ -384,9 +518,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                     }
                     sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                     sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                    const float s8 = sum * -4.76837158203125e-07f;   // -8 * 2^-24: the codes' unit
-                    q0[g][nt][0] = __shfl_sync(0xffffffffu, s8, 8 * t4);
-                    q0[g][nt][1] = __shfl_sync(0xffffffffu, s8, 8 * t4 + 4);
+                    z[g] = sum * -4.76837158203125e-07f;   // -8 * 2^-24: the codes' unit
+                }
+                // rows k = 0-3 take the first terms of the four groups, 4-7 the second, 8-11 the third
+                {
+                    const float z0 = t4 & 1 ? z[2] : z[0], z1 = t4 & 1 ? z[3] : z[1];
+                    uint32_t h, m, l;
+                    split_bf16(z0, z1, h, m);
+                    const float2 fh = bf16x2_to_float2(h);
+                    split_bf16(z0 - fh.x, z1 - fh.y, m, l);
+                    qz[nt][0] = t4 < 2 ? h : m;
+                    qz[nt][1] = t4 < 2 ? l : 0u;
                 }
                 const float mine = sl2 * __uint_as_float(uint32_t(127 + 24 - ex) << 23);
                 hs[nt][0] = __shfl_sync(0xffffffffu, mine, 8 * t4);
@@ -414,104 +556,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                 lim[nt][e] = row < nrow ? un.lim0 + row / un.heads : un.ntok;
             }
 
-        // ---- copying: lane i fetches the i-th run of R tokens of a tile
-        const int ut = p.unit_tokens;
-        int R = !INT4 ? 1 : TILE < page ? TILE : page;
-        if (sparse) while (ut % R) R >>= 1;
-        const int runs = TILE / R;
-        const int n_my = a + warp < bnd ? (bnd - a - warp + kWarps - 1) / kWarps : 0;
-        // first token of this lane's run of the j-th of my tiles, or -1
-        auto token_of = [&](int j) -> long long {
-            if (j >= n_my || lane >= runs) return -1;
-            const long long i = (long long)(a + warp + j * kWarps) * TILE + lane * R;
-            if (i >= un.ntok) return -1;
-            if (!sparse) return i;
-            const long long e = i / ut;
-            const long long n = (long long)__ldg(p.idx + size_t(un.u) * p.cap + e) * ut + (i - e * ut);
-            return n >= 0 && n < un.len ? n : -1;
-        };
-        auto page_of = [&](long long n) -> int {
-            const long long s = paged_slot(p.kv, un.b, n);
-            return s < 0 ? -1 : __ldg(p.kv.page_table + s);
-        };
-        auto issue = [&](int j, long long n, int pid) {
-            const int stage = j % STAGES;
-            const uint32_t bar = smem_u32(&s_full[warp][stage]);
-            const uint32_t dst = smem_u32(my_ring + size_t(stage) * TILE * SROW);
-            int valid = 0;                      // tokens of the run that exist
-            long long off = -1;
-            if (n >= 0) {
-                off = paged_row(p.kv, pid, un.g, n);
-                if (off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
-                else {
-                    const long long left = un.len - n;
-                    valid = left < R ? int(left) : R;
-                    if (!sparse) {
-                        const long long vis = un.ntok - n;
-                        valid = vis < valid ? int(vis) : valid;
-                    }
-                }
-            }
-            const uint32_t mask =
-                valid > 0 ? (valid >= 32 ? 0xffffffffu : ((1u << valid) - 1u)) << (lane * R) : 0u;
-            const uint32_t all = __reduce_or_sync(0xffffffffu, mask);
-            const uint32_t full = TILE == 32 ? 0xffffffffu : (1u << TILE) - 1u;
-            if (all != full) {
-                // tokens that do not exist: nothing of them may reach an operand as NaN or infinity
-                if (lane < runs)
-                    for (int i = valid; i < R; ++i) {
-                        const uint32_t row = dst + (lane * R + i) * SROW;
-                        if (INT4) sts128_zero(row + D);
-                        else
-                            for (int c = 0; c < 4 * D; c += 16) sts128_zero(row + c);
-                    }
-                asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
-            }
-            if (lane == 0) {
-                s_vmask[warp][stage] = all;
-                asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(bar),
-                             "r"(uint32_t(__popc(all) * ROWB))
-                             : "memory");
-            }
-            __syncwarp();
-            if (valid > 0)
-                asm volatile(
-                    "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
-                        dst + lane * R * SROW),
-                    "l"(p.kv.data + off), "r"(uint32_t(valid * ROWB)), "r"(bar)
-                    : "memory");
-        };
-
-        // ---- state of this warp: per column the reference m, the sum l, and O^T
-        float m_r[NT][2], l_r[NT][2], acc[DT][NT][4];
+        // ---- state of this warp: per column the reference m (-inf: no key yet), the sum l, and O^T
+        float top_r[NT][2], off_r[NT][2], l_r[NT][2], acc[DT][NT][4];   // m + kSlack and kBase - m
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            m_r[nt][0] = m_r[nt][1] = -INFINITY;
+            top_r[nt][0] = top_r[nt][1] = -INFINITY;
+            off_r[nt][0] = off_r[nt][1] = 0.f;
             l_r[nt][0] = l_r[nt][1] = 0.f;
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) acc[dt][nt][0] = acc[dt][nt][1] = acc[dt][nt][2] = acc[dt][nt][3] = 0.f;
         }
 
-        // tokens are looked up two tiles ahead of their copy and pages one ahead
-        long long n1;
-        int pg1;
-#pragma unroll
-        for (int j = 0; j < STAGES - 1; ++j)
-            if (j < n_my) {
-                const long long n = token_of(j);
-                issue(j, n, page_of(n));
-            }
-        n1 = token_of(STAGES - 1);
-        pg1 = page_of(n1);
-        long long n2 = token_of(STAGES);
+        int drain = 0;
         for (int j = 0; j < n_my; ++j) {
-            if (j + STAGES - 1 < n_my) {
-                issue(j + STAGES - 1, n1, pg1);
-                n1 = n2;
-                pg1 = page_of(n1);
-                n2 = token_of(j + STAGES + 1);
-            }
-            const int stage = j % STAGES;
+            advance();
+            const int stage = drain;
+            drain = drain + 1 == STAGES ? 0 : drain + 1;
             {
                 const uint32_t bar = smem_u32(&s_full[warp][stage]);
                 const uint32_t par = (phases >> stage) & 1u;
@@ -540,18 +600,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
             const bool edge = vmask != (TILE == 32 ? 0xffffffffu : (1u << TILE) - 1u) ||
                               (!sparse && n0 + TILE > un.lim0);
 
-            // ---- logits (in units of this kernel's q) and value scales
-            float s[MT][NT][4];
-            uint32_t vs[MT][2][2];              // 4-bit: the value scales of this lane's two tokens
-            float lgv[MT][2];                   // log2 of the largest of them
+            if constexpr (INT4) {
+                // One token per lane: its largest value scale that is a number (its bits twice: at most 2^-7 more),
+                // log2 and 1 / of it, and the scales relative to it as fp16 * 2^15, stored by token pairs over the
+                // scales themselves.
+                const uint32_t row = st + lane * SROW + D + 8;
+                const uint2 v = lds64(row);
+                const uint32_t m2 = max_bf16x2(v.x, v.y);
+                const float top = fmaxf(__uint_as_float(max_bf16x2(m2, __byte_perm(m2, m2, 0x1032))), kFloorV);
+                const float iv = __frcp_rn(top);
+                sts64(prep + lane * 8, __float_as_uint(lg2(top)), __float_as_uint(iv));
+                const uint32_t h01 = pack_f16(bf_lo(v.x) * iv * 32768.f, bf_hi(v.x) * iv * 32768.f);
+                const uint32_t h23 = pack_f16(bf_lo(v.y) * iv * 32768.f, bf_hi(v.y) * iv * 32768.f);
+                // rows 2i and 2i + 1 of a 16-row tile are a pair; the partner's token
+                const int rho = tau_inv<D, INT4>(lane & 7), mate = (lane & ~7) + tau<D, INT4>(rho ^ 1);
+                const uint32_t o01 = __shfl_sync(0xffffffffu, h01, mate), o23 = __shfl_sync(0xffffffffu, h23, mate);
+                // the first token's row takes groups 0 and 1 of both, the second's groups 2 and 3
+                if (rho & 1) sts64(row, __byte_perm(o23, h23, 0x5410), __byte_perm(o23, h23, 0x7632));
+                else sts64(row, __byte_perm(h01, o01, 0x5410), __byte_perm(h01, o01, 0x7632));
+                __syncwarp();
+            }
+            // ---- 16 tokens at a time; EDGE: some of them are not to be seen by some column
+            auto step = [&](int mt, auto edge_c) {
+                constexpr bool EDGE = decltype(edge_c)::value;
+                const int tk = mt * 16 + tau<D, INT4>(r8);
+                float s[NT][4];
+                float lgv[2] = {0.f, 0.f}, inv[2] = {1.f, 1.f};   // 4-bit: of this lane's two tokens
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int tk = mt * 16 + tau<INT4>(r8);
+                for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
                 if constexpr (INT4) {
-                    const uint32_t ra = st + tk * SROW, rb = ra + SROW;
-                    const uint4 sa = lds128(ra + D), sb = lds128(rb + D);
-                    vs[mt][0][0] = sa.z; vs[mt][0][1] = sa.w;
-                    vs[mt][1][0] = sb.z; vs[mt][1][1] = sb.w;
+                    const uint32_t ra = st + tk * SROW, rb = ra + 8 * SROW;
+                    const uint2 sa = lds64(ra + D), sb = lds64(rb + D);
+                    {
+                        // start value sum_g s_g (-8 sum q): scales (rows) by the terms of the sums
+                        const uint32_t z0 = t4 & 1 ? sa.y : sa.x, z1 = t4 & 1 ? sb.y : sb.x;
+                        const uint32_t f[4] = {z0, z1, z0, z1};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], f, qz[nt][0], qz[nt][1]);
+                    }
+                    {
+                        const uint2 wa = lds64(prep + tk * 8), wb = lds64(prep + tk * 8 + 64);
+                        lgv[0] = __uint_as_float(wa.x); inv[0] = __uint_as_float(wa.y);
+                        lgv[1] = __uint_as_float(wb.x); inv[1] = __uint_as_float(wb.y);
+                    }
                     uint32_t ka[4], kb[4];
                     if constexpr (D == 128) {
                         const uint4 wa = lds128(ra + 16 * t4), wb = lds128(rb + 16 * t4);
@@ -567,159 +658,174 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                     const float fa[4] = {bf_lo(sa.x), bf_hi(sa.x), bf_lo(sa.y), bf_hi(sa.y)};
                     const float fb[4] = {bf_lo(sb.x), bf_hi(sb.x), bf_lo(sb.y), bf_hi(sb.y)};
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
-#pragma unroll
                     for (int g = 0; g < 4; ++g) {
                         const uint32_t f0[4] = {ka[g] & 0x000f000fu, kb[g] & 0x000f000fu, ka[g] & 0x00f000f0u,
                                                 kb[g] & 0x00f000f0u};
                         const uint32_t ha = ka[g] >> 8, hb = kb[g] >> 8;
-                        const uint32_t f1[4] = {ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u,
-                                                hb & 0x00f000f0u};
+                        [[maybe_unused]] const uint32_t f1[4] = {ha & 0x000f000fu, hb & 0x000f000fu, ha & 0x00f000f0u,
+                                                                 hb & 0x00f000f0u};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            const float c[4] = {q0[g][nt][0], q0[g][nt][1], q0[g][nt][0], q0[g][nt][1]};
-                            float d[4];
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
                             if constexpr (D == 128) {
-                                mma_f16(d, f0, qb[2 * g][nt][0], qb[2 * g][nt][1], c);
-                                mma_f16(d, f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1], d);
+                                mma_f16(d, f0, qb[2 * g][nt][0], qb[2 * g][nt][1]);
+                                mma_f16(d, f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1]);
                             } else {
-                                mma_f16(d, f0, qb[g][nt][0], qb[g][nt][1], c);
+                                mma_f16(d, f0, qb[g][nt][0], qb[g][nt][1]);
                             }
-                            s[mt][nt][0] = fmaf(fa[g], d[0], s[mt][nt][0]);
-                            s[mt][nt][1] = fmaf(fa[g], d[1], s[mt][nt][1]);
-                            s[mt][nt][2] = fmaf(fb[g], d[2], s[mt][nt][2]);
-                            s[mt][nt][3] = fmaf(fb[g], d[3], s[mt][nt][3]);
+                            s[nt][0] = fmaf(fa[g], d[0], s[nt][0]);
+                            s[nt][1] = fmaf(fa[g], d[1], s[nt][1]);
+                            s[nt][2] = fmaf(fb[g], d[2], s[nt][2]);
+                            s[nt][3] = fmaf(fb[g], d[3], s[nt][3]);
                         }
-                    }
-                    // largest value scale of each token; scales are not negative, so their bits order them
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t m2 = __vmaxu2(vs[mt][e][0] & 0x7fff7fffu, vs[mt][e][1] & 0x7fff7fffu);
-                        const uint32_t m1 = max(m2 << 16, m2 & 0xffff0000u);
-                        lgv[mt][e] = lg2(fmaxf(__uint_as_float(m1), kFloorV));
                     }
                 } else {
                     const uint32_t ra = st + tk * SROW, rb = ra + 8 * SROW;
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
 #pragma unroll
                     for (int g = 0; g < D / 32; ++g) {
                         const uint4 wa = lds128(ra + g * 64 + t4 * 16), wb = lds128(rb + g * 64 + t4 * 16);
                         const uint32_t f0[4] = {wa.x, wb.x, wa.y, wb.y}, f1[4] = {wa.z, wb.z, wa.w, wb.w};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(s[mt][nt], f0, qb[2 * g][nt][0], qb[2 * g][nt][1]);
-                            mma16816(s[mt][nt], f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1]);
+                            mma16816(s[nt], f0, qb[2 * g][nt][0], qb[2 * g][nt][1]);
+                            mma16816(s[nt], f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1]);
                         }
                     }
-                    lgv[mt][0] = lgv[mt][1] = 0.f;
                 }
-            }
-            // ---- logits in log2 units, masked; the reference follows logit + log2 of the value scale
-            bool up = false;
+                // ---- the reference follows logit + log2 of the value scale
+                bool up = false;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int tk = mt * 16 + tau<INT4>(r8);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = s[mt][nt][e] * hs[nt][e & 1];
-                        if (edge) {
-                            const int tok = tk + (e >> 1) * (INT4 ? 1 : 8);
+                        s[nt][e] = fmaf(s[nt][e], hs[nt][e & 1], lgv[e >> 1]);
+                        if constexpr (EDGE) {
+                            const int tok = tk + (e >> 1) * 8;
                             const bool see = ((vmask >> tok) & 1u) && (sparse || n0 + tok < lim[nt][e & 1]);
-                            v = see ? v : -INFINITY;
-                        }
-                        s[mt][nt][e] = v;
-                        up |= v + lgv[mt][e >> 1] > m_r[nt][e & 1] + kSlack;
-                    }
-            }
-            if (__any_sync(0xffffffffu, up)) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float mx = m_r[nt][e];
-#pragma unroll
-                        for (int mt = 0; mt < MT; ++mt)
-                            mx = fmaxf(mx, fmaxf(s[mt][nt][e] + lgv[mt][0], s[mt][nt][e + 2] + lgv[mt][1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                        const float f = mx == -INFINITY ? 1.f : ex2(m_r[nt][e] - mx);
-                        m_r[nt][e] = mx;
-                        l_r[nt][e] *= f;
-#pragma unroll
-                        for (int dt = 0; dt < DT; ++dt) {
-                            acc[dt][nt][e] *= f;
-                            acc[dt][nt][e + 2] *= f;
+                            s[nt][e] = see ? s[nt][e] : -INFINITY;
                         }
                     }
-            }
-            // ---- weights and O^T += V^T W^T
+                    up |= fmaxf(s[nt][0], s[nt][2]) > top_r[nt][0] || fmaxf(s[nt][1], s[nt][3]) > top_r[nt][1];
+                }
+                if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                        for (int e = 0; e < 2; ++e) {
+                            const float old = top_r[nt][e] - kSlack;
+                            float mx = fmaxf(old, fmaxf(s[nt][e], s[nt][e + 2]));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                            const float f = mx == -INFINITY ? 1.f : ex2(old - mx);
+                            top_r[nt][e] = mx + kSlack;
+                            off_r[nt][e] = mx == -INFINITY ? 0.f : kBase - mx;
+                            l_r[nt][e] *= f;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float m = m_r[nt][e & 1];   // still -inf: every logit is -inf, or NaN (kept)
-                        const float pr = ex2(s[mt][nt][e] - (m == -INFINITY ? 0.f : m) + kBase);
-                        s[mt][nt][e] = pr;
-                        l_r[nt][e & 1] += pr;
-                    }
-                if constexpr (INT4) {
-                    // value codes of this lane's fragment row for the tokens of k = 2 t4, 2 t4 + 1 (+ 8)
-                    const int ta = mt * 16 + tau<INT4>(2 * t4), tb = mt * 16 + tau<INT4>(2 * t4 + 1);
-                    const uint32_t vb = st + D / 2 + r8 * (D / 16);
-                    uint32_t va[2], vbw[2], vc[2], vd[2];
-                    if constexpr (D == 128) {
-                        uint2 w;
-                        w = lds64(vb + ta * SROW); va[0] = w.x; va[1] = w.y;
-                        w = lds64(vb + tb * SROW); vbw[0] = w.x; vbw[1] = w.y;
-                        w = lds64(vb + (ta + 1) * SROW); vc[0] = w.x; vc[1] = w.y;
-                        w = lds64(vb + (tb + 1) * SROW); vd[0] = w.x; vd[1] = w.y;
-                    } else {
-                        va[0] = lds32(vb + ta * SROW); vbw[0] = lds32(vb + tb * SROW);
-                        vc[0] = lds32(vb + (ta + 1) * SROW); vd[0] = lds32(vb + (tb + 1) * SROW);
-                    }
-                    constexpr int BPG = D / 64;   // bytes, and 16-channel tiles, per group
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        uint32_t b0[NT], b1[NT];
-                        const uint32_t sa = vs[mt][0][g >> 1], sb = vs[mt][1][g >> 1];
-                        const float fa = g & 1 ? bf_hi(sa) : bf_lo(sa), fb = g & 1 ? bf_hi(sb) : bf_lo(sb);
+                            for (int dt = 0; dt < DT; ++dt) {
+                                acc[dt][nt][e] *= f;
+                                acc[dt][nt][e + 2] *= f;
+                            }
+                        }
+                }
+                // Tokens that some of the queries do not see: one product per query token, with the values it does
+                // not see taken as 0 (0 * NaN would reach its sum).
+                auto edge_product = [&](const uint32_t (&f)[4], int dt, auto product) {
+                    const int ka = n0 + mt * 16 + tau<D, INT4>(2 * t4), kb = n0 + mt * 16 + tau<D, INT4>(2 * t4 + 1);
+                    for (int i = 0; i < un.nq; ++i) {
+                        const int sees = un.lim0 + i;
+                        const uint32_t mlo = (ka < sees ? 0xffffu : 0u) | (kb < sees ? 0xffff0000u : 0u);
+                        const uint32_t mhi = (ka + 8 < sees ? 0xffffu : 0u) | (kb + 8 < sees ? 0xffff0000u : 0u);
+                        const uint32_t fi[4] = {f[0] & mlo, f[1] & mlo, f[2] & mhi, f[3] & mhi};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            float w[4] = {s[mt][nt][0] * fa, s[mt][nt][1] * fa, s[mt][nt][2] * fb, s[mt][nt][3] * fb};
-                            if (edge) {   // a masked token's scale may be NaN: its weight is 0, not 0 * NaN
+                            float o[4] = {0.f, 0.f, 0.f, 0.f};
+                            product(nt, o, fi);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) w[e] = s[mt][nt][e] == 0.f ? 0.f : w[e];
-                            }
-                            b0[nt] = movm_t(pack_f16(w[0], w[1]));
-                            b1[nt] = movm_t(pack_f16(w[2], w[3]));
+                            for (int e = 0; e < 4; ++e)
+                                if ((nt * 8 + 2 * t4 + (e & 1)) / un.heads == i) acc[dt][nt][e] += o[e];
                         }
+                    }
+                };
+                (void)edge_product;
+                // ---- weights and O^T += V^T P^T
 #pragma unroll
-                        for (int i = 0; i < BPG; ++i) {
-                            const int by = g * BPG + i;          // byte of the row's share
-                            const uint32_t sel = uint32_t(by & 3) | (uint32_t(4 + (by & 3)) << 8);
-                            const uint32_t lo = __byte_perm(va[by >> 2], vbw[by >> 2], sel);
-                            const uint32_t hi = __byte_perm(vc[by >> 2], vd[by >> 2], sel);
-                            // u * 2^-24 (or 2^-20) minus 8 of the same unit: exact
-                            const uint32_t f[4] = {sub_f16x2(lo & 0x000f000fu, 0x00080008u),
-                                                   sub_f16x2(lo & 0x00f000f0u, 0x00800080u),
-                                                   sub_f16x2(hi & 0x000f000fu, 0x00080008u),
-                                                   sub_f16x2(hi & 0x00f000f0u, 0x00800080u)};
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma_f16(acc[by][nt], f, b0[nt], b1[nt], acc[by][nt]);
+                    for (int e = 0; e < 4; ++e) {
+                        s[nt][e] = ex2(s[nt][e] + off_r[nt][e & 1]);
+                        l_r[nt][e & 1] = INT4 ? fmaf(s[nt][e], inv[e >> 1], l_r[nt][e & 1]) : l_r[nt][e & 1] + s[nt][e];
+                    }
+                if constexpr (INT4) {
+                    uint32_t b0[NT], b1[NT];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        b0[nt] = movm_t(pack_f16(s[nt][0], s[nt][1]));
+                        b1[nt] = movm_t(pack_f16(s[nt][2], s[nt][3]));
+                    }
+                    // This lane's codes belong to one group (d = 128) or two (d = 64: codes 0, 1 and 2, 3 of a
+                    // unit).  Its r_g * 2^15 for the token pairs of k = 2 t4, 2 t4 + 1 and the same + 8 lie where
+                    // the two tokens had their value scales: groups 0, 1 in the first token's row, 2, 3 in the
+                    // second's.
+                    constexpr int NG = D == 128 ? 1 : 2;
+                    uint32_t rg[2][NG], nl[2][NG], nh[2][NG];   // r, and -8 r in the units of the two kinds of codes
+                    {
+                        const int g0 = D == 128 ? r8 & 3 : 2 * (r8 & 1);
+                        const uint32_t at = st + (mt * 16 + tau<D, INT4>(2 * t4 + (g0 >> 1))) * SROW + D + 8 + (g0 & 1) * 4;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if constexpr (NG == 1) {
+                                rg[h][0] = lds32(at + h * 8 * SROW);
+                            } else {
+                                const uint2 w = lds64(at + h * 8 * SROW);
+                                rg[h][0] = w.x;
+                                rg[h][1] = w.y;
+                            }
+#pragma unroll
+                            for (int i = 0; i < NG; ++i) {
+                                nl[h][i] = mul_f16x2(rg[h][i], 0x80408040u);   // -8 * 2^-21
+                                nh[h][i] = mul_f16x2(rg[h][i], 0x84008400u);   // -8 * 2^-17
+                            }
+                        }
+                    }
+                    // 16-bit units of V transposed: matrices (chunk q, tokens 0-7), (chunk q, tokens 8-15), ...
+                    const uint32_t vb =
+                        st + (mt * 16 + tau<D, INT4>(lane & 7) + ((lane >> 3) & 1) * 8) * SROW + D / 2 + (lane >> 4) * 16;
+#pragma unroll
+                    for (int qq = 0; qq < D / 64; ++qq) {
+                        uint32_t x[4];
+                        ldsm_x4_t(vb + qq * 32, x[0], x[1], x[2], x[3]);
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {       // codes 2e and 2e + 1 of the units
+                                // a code in bits 3-6 is u * 2^-21 as fp16, in bits 7-10 u * 2^-17 (bit 10 is the
+                                // exponent's lowest, whose step is the denormals'): products stay above 2^-6 r
+                                const uint32_t lo = e ? x[2 * q] >> 5 : x[2 * q] << 3;
+                                const uint32_t hi = e ? x[2 * q + 1] >> 5 : x[2 * q + 1] << 3;
+                                const int i = NG == 1 ? 0 : e;
+                                const uint32_t f[4] = {fma_f16x2(lo & 0x00780078u, rg[0][i], nl[0][i]),
+                                                       fma_f16x2(lo & 0x07800780u, rg[0][i], nh[0][i]),
+                                                       fma_f16x2(hi & 0x00780078u, rg[1][i], nl[1][i]),
+                                                       fma_f16x2(hi & 0x07800780u, rg[1][i], nh[1][i])};
+                                const int dt = (2 * qq + q) * 2 + e;
+                                if (!EDGE || un.nq == 1) {
+#pragma unroll
+                                    for (int nt = 0; nt < NT; ++nt) mma_f16(acc[dt][nt], f, b0[nt], b1[nt]);
+                                } else {
+                                    edge_product(f, dt, [&](int nt, float (&o)[4], const uint32_t (&fi)[4]) {
+                                        mma_f16(o, fi, b0[nt], b1[nt]);
+                                    });
+                                }
+                            }
                         }
                     }
                 } else {
                     uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
-                        split_bf16(s[mt][nt][0], s[mt][nt][1], ph[nt][0], pl[nt][0]);
-                        split_bf16(s[mt][nt][2], s[mt][nt][3], ph[nt][1], pl[nt][1]);
+                        split_bf16(s[nt][0], s[nt][1], ph[nt][0], pl[nt][0]);
+                        split_bf16(s[nt][2], s[nt][3], ph[nt][1], pl[nt][1]);
                         ph[nt][0] = movm_t(ph[nt][0]);
                         ph[nt][1] = movm_t(ph[nt][1]);
                         pl[nt][0] = movm_t(pl[nt][0]);
@@ -727,46 +833,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                     }
                     // V^T tile dt: a0 = channels 0-7 x k 0-7, a1 = channels 8-15 x k 0-7, a2, a3 = k 8-15
                     const int mat = lane >> 3;
-                    const int tk = mt * 16 + tau<INT4>(lane & 7) + (mat >> 1) * 8;
-                    const uint32_t vb = st + tk * SROW + 2 * D + (mat & 1) * 16;
-                    if (!edge || un.nq == 1) {
+                    const int tv = mt * 16 + tau<D, INT4>(lane & 7) + (mat >> 1) * 8;
+                    const uint32_t vb = st + tv * SROW + 2 * D + (mat & 1) * 16;
 #pragma unroll
-                        for (int dt = 0; dt < DT; ++dt) {
-                            uint32_t f[4];
-                            ldsm_x4_t(vb + dt * 32, f[0], f[1], f[2], f[3]);
+                    for (int dt = 0; dt < DT; ++dt) {
+                        uint32_t f[4];
+                        ldsm_x4_t(vb + dt * 32, f[0], f[1], f[2], f[3]);
+                        if (!EDGE || un.nq == 1) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 mma16816(acc[dt][nt], f, ph[nt][0], ph[nt][1]);
                                 mma16816(acc[dt][nt], f, pl[nt][0], pl[nt][1]);
                             }
-                        }
-                    } else {
-                        // Tokens that some of the queries do not see: one product per query token, with the
-                        // values it does not see taken as 0 (0 * NaN would reach its sum).
-                        const int ka = n0 + mt * 16 + tau<INT4>(2 * t4), kb = n0 + mt * 16 + tau<INT4>(2 * t4 + 1);
-                        for (int i = 0; i < un.nq; ++i) {
-                            const int sees = un.lim0 + i;
-                            const uint32_t mlo = (ka < sees ? 0xffffu : 0u) | (kb < sees ? 0xffff0000u : 0u);
-                            const uint32_t mhi = (ka + 8 < sees ? 0xffffu : 0u) | (kb + 8 < sees ? 0xffff0000u : 0u);
-#pragma unroll
-                            for (int dt = 0; dt < DT; ++dt) {
-                                uint32_t f[4];
-                                ldsm_x4_t(vb + dt * 32, f[0], f[1], f[2], f[3]);
-                                f[0] &= mlo; f[1] &= mlo; f[2] &= mhi; f[3] &= mhi;
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    float o[4] = {0.f, 0.f, 0.f, 0.f};
-                                    mma16816(o, f, ph[nt][0], ph[nt][1]);
-                                    mma16816(o, f, pl[nt][0], pl[nt][1]);
-#pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        if ((nt * 8 + 2 * t4 + (e & 1)) / un.heads == i) acc[dt][nt][e] += o[e];
-                                }
-                            }
+                        } else {
+                            edge_product(f, dt, [&](int nt, float (&o)[4], const uint32_t (&fi)[4]) {
+                                mma16816(o, fi, ph[nt][0], ph[nt][1]);
+                                mma16816(o, fi, pl[nt][0], pl[nt][1]);
+                            });
                         }
                     }
                 }
+            };
+            if (edge) {
+#pragma unroll 1
+                for (int mt = 0; mt < MT; ++mt) step(mt, std::true_type{});
+            } else {
+#pragma unroll 1
+                for (int mt = 0; mt < MT; ++mt) step(mt, std::false_type{});
             }
+            if constexpr (INT4) asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // the pair scales
             __syncwarp();   // every lane has read the stage before it is filled again
         }
 
@@ -781,42 +876,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                 l += __shfl_xor_sync(0xffffffffu, l, 4);
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
-                float* const rec = mg + (warp * kRowsMax + nt * 8 + 2 * t4 + e) * (D + 2);
+                float* const rec = mg + (warp * ROWS + nt * 8 + 2 * t4 + e) * (D + 2);
 #pragma unroll
                 for (int dt = 0; dt < DT; ++dt) {
-                    // codes are in units of 2^-24, and of 2^-20 in the upper eight channels
-                    rec[dt * 16 + r8] = acc[dt][nt][e] * (INT4 ? 16777216.f : 1.f);
-                    rec[dt * 16 + r8 + 8] = acc[dt][nt][e + 2] * (INT4 ? 1048576.f : 1.f);
+                    if constexpr (INT4) {   // tile dt: chunk dt / 2, codes 2 (dt % 2) and the next of its units
+                        const int q = dt >> 1, e2 = 2 * (dt & 1);
+                        const int c0 = D == 128 ? 32 * (r8 & 3) + 2 * q + (r8 >> 2) + 8 * e2
+                                                : 16 * (2 * (r8 & 1) + (dt & 1)) + 4 * q + (r8 >> 1);
+                        rec[c0] = acc[dt][nt][e] * 64.f;        // values were held times 2^-6 and 2^-2
+                        rec[c0 + 8] = acc[dt][nt][e + 2] * 4.f;
+                    } else {
+                        rec[dt * 16 + r8] = acc[dt][nt][e];
+                        rec[dt * 16 + r8 + 8] = acc[dt][nt][e + 2];
+                    }
                 }
                 if (r8 == 0) {
-                    rec[D] = m_r[nt][e];
+                    rec[D] = top_r[nt][e] - kSlack;
                     rec[D + 1] = l;
                 }
             }
         __syncthreads();
-        const bool whole = a == 0 && bnd == tiles;
+        const bool whole = a == 0 && bnd == int(s_seg[1] - s_seg[0]) - kSeg;
+        auto store = [&](int row, int c, float M, float L, float O) {
+            const float val = L == 0.f ? 0.f : O / L;
+            const size_t orow = size_t(un.row0 + row / un.heads) * p.Hq + un.h0 + row % un.heads;
+            const __nv_bfloat16 bv = __float2bfloat16_rn(val);
+            p.out[orow * D + c] = *reinterpret_cast<const uint16_t*>(&bv);
+            if (p.out_f32) p.out_f32[orow * D + c] = val;
+            if (p.lse && c == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M - kBase + log2f(L)) * kLn2;
+        };
         // a unit's first share goes to slot 2c + 1 of its CTA, later shares to slot 2c
-        float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * kRowsMax * (D + 2);
+        constexpr int REC = kRowsMax * (D + 2);
+        float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
         for (int i = tid; i < nrow * D; i += kThreads) {
             const int row = i / D, c = i % D;
             float M = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg[(w * kRowsMax + row) * (D + 2) + D]);
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg[(w * ROWS + row) * (D + 2) + D]);
             float L = 0.f, O = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float* rec = mg + (w * kRowsMax + row) * (D + 2);
+                const float* rec = mg + (w * ROWS + row) * (D + 2);
                 const float f = rec[D] == -INFINITY ? 0.f : ex2(rec[D] - M);
-                L += rec[D + 1] * f;
+                L += rec[D + 1] * f;   // a warp that saw only NaN has m = -inf and keeps its NaN here
                 O += rec[c] * f;
             }
             if (whole) {
-                const float val = L == 0.f ? 0.f : O / L;
-                const size_t orow = size_t(un.row0 + row / un.heads) * p.Hq + un.h0 + row % un.heads;
-                const __nv_bfloat16 bv = __float2bfloat16_rn(val);
-                p.out[orow * D + c] = *reinterpret_cast<const uint16_t*>(&bv);
-                if (p.out_f32) p.out_f32[orow * D + c] = val;
-                if (p.lse && c == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M - kBase + log2f(L)) * kLn2;
+                store(row, c, M, L, O);
             } else {
                 part[row * (D + 2) + c] = O;
                 if (c == 0) {
@@ -825,57 +931,81 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_kernel(PagedAttendPa
                 }
             }
         }
-        if (!whole && a == 0 && tid == 0)
-            p.split[cta] = make_int4(un.row0, un.h0, un.heads | (nrow << 8),
-                                     paged_tile_owner(u_hi - 1, TT, GC));
+        if (!whole) {
+            // the last CTA of a split unit to get here merges its partials, in the order of the CTAs
+            const long long tt = s_prefix[groups];
+            const int lo = paged_tile_owner(s_seg[0] + kSeg, tt, GC), hi = paged_tile_owner(s_seg[1] - 1, tt, GC);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int n = atomicAdd(p.arrived + lo, 1);
+                s_last = n == hi - lo;
+                if (n == hi - lo) p.arrived[lo] = 0;   // ready for the next call
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                const float* const base = p.partials + size_t(2 * lo + 1) * REC;   // slot of CTA lo, then 2k
+                const int n = hi - lo + 1;
+                float* const fac = mg;                     // [nrow][n]: factor of every partial; then M and L
+                float* const ml = mg + nrow * n;
+                auto slot = [&](int k) { return k == 0 ? base : base + size_t(2 * k - 1) * REC; };
+                for (int row = warp; row < nrow; row += kWarps) {
+                    float M = -INFINITY;
+                    for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(slot(k) + row * (D + 2) + D));
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+                    float L = 0.f;
+                    for (int k = lane; k < n; k += 32) {
+                        const float m = __ldcg(slot(k) + row * (D + 2) + D);
+                        const float f = m == -INFINITY ? 0.f : ex2(m - M);
+                        fac[row * n + k] = f;
+                        L += f * __ldcg(slot(k) + row * (D + 2) + D + 1);
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                    if (lane == 0) {
+                        ml[2 * row] = M;
+                        ml[2 * row + 1] = L;
+                    }
+                }
+                __syncthreads();
+                for (int i = tid; i < nrow * D; i += kThreads) {
+                    const int row = i / D, c = i % D;
+                    float O = 0.f;
+#pragma unroll 8
+                    for (int k = 0; k < n; ++k) {
+                        const float f = fac[row * n + k], o = __ldcg(slot(k) + row * (D + 2) + c);
+                        O += f * o;
+                    }
+                    store(row, c, ml[2 * row], ml[2 * row + 1], O);
+                }
+            }
+        }
         asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");   // before the ring is copied into again
         __syncthreads();
         if (bad && tid == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
-        x = x_next;
+        x = s_seg[2];
+        __syncthreads();
     }
-}
-
-// Merge of a split unit's partials, in the order of their CTAs: block (c, row) takes row `row` of the unit
-// that starts in CTA c and goes on past it.
-template <int D>
-__global__ void __launch_bounds__(D) paged_combine_kernel(PagedAttendParams p) {
-    pdl_enter();
-    const int c0 = blockIdx.x, row = blockIdx.y, c = threadIdx.x;
-    const int4 s = p.split[c0];
-    const int heads = s.z & 255, nrow = s.z >> 8, hi = s.w;
-    if (s.x < 0 || row >= nrow) return;
-    const size_t rec = D + 2;
-    const float* const first = p.partials + (size_t(2 * c0 + 1) * kRowsMax + row) * rec;
-    auto slot = [&](int k) { return k == c0 ? first : p.partials + (size_t(2 * k) * kRowsMax + row) * rec; };
-    float M = -INFINITY;
-    for (int k = c0; k <= hi; ++k) M = fmaxf(M, __ldcg(slot(k) + D));
-    float L = 0.f, O = 0.f;
-#pragma unroll 4
-    for (int k = c0; k <= hi; ++k) {
-        const float* r = slot(k);
-        const float m = __ldcg(r + D);
-        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-        L += __ldcg(r + D + 1) * f;
-        O += __ldcg(r + c) * f;
-    }
-    const float val = L == 0.f ? 0.f : O / L;
-    const size_t orow = size_t(s.x + row / heads) * p.Hq + s.y + row % heads;
-    const __nv_bfloat16 bv = __float2bfloat16_rn(val);
-    p.out[orow * D + c] = *reinterpret_cast<const uint16_t*>(&bv);
-    if (p.out_f32) p.out_f32[orow * D + c] = val;
-    if (p.lse && c == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M - kBase + log2f(L)) * kLn2;
 }
 
 }  // namespace
 
+// Workspace after the header: [2 * SMs] arrival counters, then two partials of 16 rows for each CTA.
+static size_t paged_attend_grid_max() { return size_t(device_info().num_sms) * 2; }
 size_t paged_attend_scratch_bytes(int d) {
-    const size_t grid = device_info().num_sms;
-    return align_up(grid * sizeof(int4), 256) + align_up(2 * grid * kRowsMax * (d + 2) * 4, 256);
+    const size_t grid = paged_attend_grid_max();
+    return align_up(grid * 4, 256) + align_up(2 * grid * kRowsMax * (d + 2) * 4, 256);
+}
+void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch) {
+    p.arrived = reinterpret_cast<int*>(scratch);
+    p.partials = reinterpret_cast<float*>(scratch + align_up(paged_attend_grid_max() * 4, 256));
 }
 
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
     const int G = p.Hq / p.kv.Hkv;
-    const int grid = device_info().num_sms;
+    const int sms = device_info().num_sms;
     const bool sparse = p.idx != nullptr;
     const int heads = sparse && p.collapse == SPA_COLLAPSE_NONE ? 1 : G;
     if (heads > kRowsMax) return SPA_ERR_UNSUPPORTED_SHAPE;
@@ -884,22 +1014,28 @@ spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
     const int TQ = sparse || p.T <= p.kv.B ? 1 : paged_tokens_per_tile(kRowsMax, G);
     const int nt = TQ * heads > 8 ? 2 : 1;
     // the prefix of a launch's groups lies in shared memory, so a launch takes at most kPagedMaxUnits of them
-    for (long long g0 = 0; g0 < all; g0 += kPagedMaxUnits) {
-        const int groups = int(all - g0 < kPagedMaxUnits ? all - g0 : kPagedMaxUnits);
+    // (and the weighted tiles of a launch are counted in 32 bits: a sequence's queries times its length bound them)
+    const long long tiles = (((long long)p.kv.max_pages << p.kv.page_shift) + 15) / 16 + kSeg;
+    const long long most = sparse ? ((long long)p.cap * p.unit_tokens + 15) / 16 + kSeg
+                                  : tiles * p.kv.Hkv * ((p.T + TQ - 1) / TQ);
+    long long step = kPagedMaxUnits;
+    if (!sparse && most + tiles * p.kv.Hkv * step > 0xffffffffll) step = (0xffffffffll - most) / (tiles * p.kv.Hkv);
+    if (sparse && most * step > 0xffffffffll) step = 0xffffffffll / most;
+    if (step < 1) return SPA_ERR_UNSUPPORTED_SHAPE;
+    for (long long g0 = 0; g0 < all; g0 += step) {
+        const int groups = int(all - g0 < step ? all - g0 : step);
 #define SPA_PA(DD, I4, NTT)                                                                                      \
     if (p.kv.d == DD && (p.kv.int4 != 0) == I4 && nt == NTT) {                                                   \
-        constexpr size_t kMost = Geo<DD, I4>::SMEM + size_t(kPagedMaxUnits + 1) * 8;                             \
+        using G_ = Geo<DD, I4, NTT>;                                                                             \
+        constexpr size_t kMost = G_::SMEM + size_t(kPagedMaxUnits + 1) * 4;                                      \
         SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_attend_kernel<DD, I4, NTT>),              \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)));                   \
-        SPA_CUDA_TRY(launch_pdl(paged_attend_kernel<DD, I4, NTT>, dim3(grid), dim3(kThreads),                    \
-                                Geo<DD, I4>::SMEM + size_t(groups + 1) * 8, st, p, int(g0), groups, TQ));        \
+        SPA_CUDA_TRY(launch_pdl(paged_attend_kernel<DD, I4, NTT>, dim3(sms * G_::CTAS), dim3(G_::WARPS * 32),    \
+                                G_::SMEM + size_t(groups + 1) * 4, st, p, int(g0), groups, TQ));                 \
     }
         SPA_PA(64, false, 1) SPA_PA(64, false, 2) SPA_PA(64, true, 1) SPA_PA(64, true, 2)
         SPA_PA(128, false, 1) SPA_PA(128, false, 2) SPA_PA(128, true, 1) SPA_PA(128, true, 2)
 #undef SPA_PA
-        const dim3 rows(grid, nt * 8);
-        if (p.kv.d == 64) SPA_CUDA_TRY(launch_pdl(paged_combine_kernel<64>, rows, dim3(64), 0, st, p));
-        else SPA_CUDA_TRY(launch_pdl(paged_combine_kernel<128>, rows, dim3(128), 0, st, p));
     }
     return SPA_OK;
 }

@@ -5,7 +5,8 @@ Tolerances, derived from the formats before any run:
   rotation (three roundings and two of cos and sin: 4 * 2^-24 of |x| + |y|);
 - a 4-bit value is within scale / 2 of the exact one (plus the same rotation error), its scale the exact
   amax / 7 rounded up to bf16 from a binary32 amax;
-- attention: weights are off by 2^-11 (4-bit: rounded to fp16) or 2^-15 (bf16: hi + lo), logits by
+- attention: weights are off by 3 * 2^-11 (4-bit: the weight, the group's scale relative to its token's largest,
+  and their product with the code are rounded to fp16 once each) or 2^-15 (bf16: hi + lo), logits by
   delta = 128 * 2^-23 of the sum of the products' magnitudes (binary32 accumulation in any order, codes
   unsigned up to 15), which scales weights by e^(2 delta); outputs by their final rounding.
 """
@@ -99,13 +100,16 @@ def check_attention(c, q, out, lse, sees, sm_scale, b, what):
             delta = sm_scale * mag * 128 * 2.0**-23 + 2.0**-20
             p = np.exp(Ks @ q[h] * sm_scale - z)
             av = p @ np.abs(c.V[b][g][s])
-            tol = np.abs(o) * 2.0**-8 + (2 * delta + (2.0**-11 if c.fmt == INT4 else 2.0**-15)) * av * 1.01 + 1e-30
+            tol = np.abs(o) * 2.0**-8 + (2 * delta + (3 * 2.0**-11 if c.fmt == INT4 else 2.0**-15)) * av * 1.01 + 1e-30
             if c.fmt == INT4:
-                # fp16 has an absolute floor: weights W = p * s are held in units in which the largest p * (largest
-                # value scale of its token) is at least 2^9, and below 2^-14 round to multiples of 2^-24, so each is
-                # off by at most 2^-25 / 2^9 = 2^-34 of that largest product; a code is at most 8 in magnitude, which
-                # makes n * 2^-31 of it over n tokens.
-                tol = tol + len(p) * 2.0**-31 * (p * c.vs[b][g][s].max(-1)).max()
+                # fp16 has an absolute floor, multiples of 2^-24.  Weights P = p * (their token's largest value scale)
+                # are held in units in which the largest is at least 2^9, so below the floor each is off by at most
+                # 2^-25 / 2^9 = 2^-34 of that largest; a code is at most 8 in magnitude: n * 2^-31 of it over n
+                # tokens.  A value relative to its token's largest scale is held times 2^-6 at least, so below the
+                # floor it is off by 2^-25 * 2^6 = 2^-19 of that scale; a relative scale is held times 2^15 and is
+                # off by 2^-40, times a code of at most 8.
+                big = p * c.vs[b][g][s].max(-1)
+                tol = tol + len(p) * 2.0**-31 * big.max() + (2.0**-19 + 2.0**-37) * big.sum()
             err = np.abs(out[h] - o)
             assert (err <= tol).all(), f"{what}: head {h}, out off by {(err / tol).max():.2f} of the tolerance"
             assert abs(lse[h] - z) <= delta + 2.0**-21 * max(abs(z), 32), f"{what}: head {h}, lse {lse[h]} vs {z}"
@@ -438,6 +442,43 @@ def test_value_scales_that_differ_between_tokens():
         for b in range(2):
             check_attention(c, _bf(q)[b], _bf(plan.out)[b], _np(plan.lse)[b].astype(np.float64), [np.ones(64, bool)],
                             scale, b, f"scale {scale}")
+
+
+def test_value_scales_that_differ_within_a_token():
+    c = Cache([100], 1, 128, 16, INT4, seed=14)
+    rng = np.random.default_rng(14)
+    for n in range(100):
+        k = rng.standard_normal((1, 1, 128)).astype(np.float32)
+        v = rng.standard_normal((1, 1, 128)) * np.repeat(2.0 ** rng.integers(-12, 13, 4), 32)
+        v[0, 0, :32] *= n % 7 != 3           # and groups that are zero
+        row = ref.pack(k, v.astype(np.float32))
+        c.pool[c.table[0, n // 16], :, n % 16] = torch.from_numpy(row[:, 0]).cuda()
+        K, V, ks, vs = ref.unpack(row)
+        c.K[0][:, n], c.V[0][:, n], c.ks[0][:, n], c.vs[0][:, n] = K[:, 0], V[:, 0], ks[:, 0], vs[:, 0]
+    q = torch.randn(1, 8, 128, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, **c.kw)
+    check_attention(c, _bf(q)[0], _bf(plan.out)[0], _np(plan.lse)[0].astype(np.float64), [np.ones(100, bool)], 0.1, 0,
+                    "groups")
+
+
+@pytest.mark.parametrize("fmt,d", [(INT4, 128), (INT4, 64), (BF16, 128)])
+def test_a_value_that_is_not_finite_reaches_its_channels_and_no_others(fmt, d):
+    c = Cache([70, 70], 1, d, 16, fmt, seed=15)
+    host = c.pool.view(torch.uint8).reshape(c.pool.shape[0], 1, 16, -1)
+    for b in range(2):                      # one group (4-bit) or one channel (bf16) of one token's value, and of all
+        for n in ([33] if b == 0 else range(70)):
+            at = slice(d + 8 + 4, d + 8 + 6) if fmt == INT4 else slice(2 * d + 80, 2 * d + 82)
+            host[c.table[b, n // 16], 0, n % 16, at] = torch.tensor([0xC0, 0x7F], dtype=torch.uint8, device="cuda")
+    q = torch.randn(2, 4, d, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, **c.kw)
+    out, lse = _bf(plan.out), _np(plan.lse).astype(np.float64)
+    hit = np.zeros(d, bool)
+    hit[slice(d // 2, 3 * d // 4) if fmt == INT4 else slice(40, 41)] = True
+    assert np.isnan(out[:, :, hit]).all() and np.isfinite(out[:, :, ~hit]).all() and np.isfinite(lse).all()
+    c.V[0][:, :, hit] = c.V[1][:, :, hit] = 0
+    out[:, :, hit] = 0
+    for b in range(2):
+        check_attention(c, _bf(q)[b], out[b], lse[b], [np.ones(70, bool)], 0.1, b, "other channels")
 
 
 def test_attend_reports_bad_pages_and_skips_them():
