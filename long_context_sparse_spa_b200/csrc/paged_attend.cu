@@ -38,7 +38,7 @@ namespace spa {
 namespace {
 
 constexpr int kRowsMax = 16;              // (query, head) rows of a unit
-constexpr int kSeg = 8;                   // tiles charged to a unit for its start-up and merge
+constexpr int kSeg = 32;                  // tiles charged to a unit for its start-up and merge
 constexpr int kShare = 16;                // least weighted tiles of a CTA's share
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -46,6 +46,9 @@ constexpr float kFloorV = 8.077935669463161e-28f;   // 2^-90: least value scale 
 constexpr float kBase = 9.f;              // weights are 2^9 at the reference, and at most 2^(9 + kSlack)
 constexpr float kSlack = 6.f;             // the reference moves only when it is exceeded by this (log2)
 constexpr uint32_t kWaitLimit = 1u << 22;
+
+// floats of one share of a split unit
+__host__ __device__ constexpr int paged_rec_floats(int d) { return kRowsMax * (d + 2); }
 
 template <int D, bool INT4, int NT>
 struct Geo {
@@ -59,7 +62,8 @@ struct Geo {
     // the eight rows of a fragment on the same banks)
     static constexpr int SROW = INT4 ? ROWB : ROWB + 16;
     static constexpr int RING = WARPS * STAGES * TILE * SROW;
-    static constexpr int MERGE = WARPS * NT * 8 * (D + 2) * 4;
+    // the warps' parts, their factors and (M, L); the merge of shares puts a factor of each over the parts
+    static constexpr int MERGE = WARPS * NT * 8 * (D + 2) * 4 + NT * 8 * (WARPS + 2) * 4;
     static constexpr int PREP = INT4 ? WARPS * TILE * 8 : 0;   // (log2, 1 / value) of each token's largest value scale
     static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + PREP;
 };
@@ -897,42 +901,62 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
             }
         __syncthreads();
         const bool whole = a == 0 && bnd == int(s_seg[1] - s_seg[0]) - kSeg;
-        auto store = [&](int row, int c, float M, float L, float O) {
-            const float val = L == 0.f ? 0.f : O / L;
-            const size_t orow = size_t(un.row0 + row / un.heads) * p.Hq + un.h0 + row % un.heads;
-            const __nv_bfloat16 bv = __float2bfloat16_rn(val);
-            p.out[orow * D + c] = *reinterpret_cast<const uint16_t*>(&bv);
-            if (p.out_f32) p.out_f32[orow * D + c] = val;
-            if (p.lse && c == 0) p.lse[orow] = L == 0.f ? -INFINITY : (M - kBase + log2f(L)) * kLn2;
+        // four channels of a row
+        auto store = [&](int row, int c, float L, float4 o) {
+            const float il = L == 0.f ? 0.f : 1.f / L;   // L == 0: nothing seen
+            const size_t at = (size_t(un.row0 + row / un.heads) * p.Hq + un.h0 + row % un.heads) * D + c;
+            o = make_float4(o.x * il, o.y * il, o.z * il, o.w * il);
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
+            *reinterpret_cast<uint2*>(p.out + at) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + at) = o;
         };
-        // a unit's first share goes to slot 2c + 1 of its CTA, later shares to slot 2c
-        constexpr int REC = kRowsMax * (D + 2);
-        float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
-        for (int i = tid; i < nrow * D; i += kThreads) {
-            const int row = i / D, c = i % D;
-            float M = -INFINITY;
+        auto store_lse = [&](int row, float M, float L) {
+            if (p.lse)
+                p.lse[size_t(un.row0 + row / un.heads) * p.Hq + un.h0 + row % un.heads] =
+                    L == 0.f ? -INFINITY : (M - kBase + log2f(L)) * kLn2;
+        };
+        // per row: the factor of every warp's (later: every share's) part, and the row's (M, L)
+        float* const fac = mg + kWarps * ROWS * (D + 2);
+        float* const ml = fac + ROWS * kWarps;
+        if (tid < nrow) {
+            float M = -INFINITY, L = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg[(w * ROWS + row) * (D + 2) + D]);
-            float L = 0.f, O = 0.f;
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mg[(w * ROWS + tid) * (D + 2) + D]);
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float* rec = mg + (w * ROWS + row) * (D + 2);
+                const float* rec = mg + (w * ROWS + tid) * (D + 2);
                 const float f = rec[D] == -INFINITY ? 0.f : ex2(rec[D] - M);
+                fac[tid * kWarps + w] = f;
                 L += rec[D + 1] * f;   // a warp that saw only NaN has m = -inf and keeps its NaN here
-                O += rec[c] * f;
             }
-            if (whole) {
-                store(row, c, M, L, O);
-            } else {
-                part[row * (D + 2) + c] = O;
-                if (c == 0) {
-                    part[row * (D + 2) + D] = M;
-                    part[row * (D + 2) + D + 1] = L;
-                }
+            ml[2 * tid] = M;
+            ml[2 * tid + 1] = L;
+        }
+        __syncthreads();
+        // A unit's first share goes to slot 2c + 1 of its CTA, later shares to slot 2c.  A slot holds O [16][D],
+        // then (M, L) [16].
+        constexpr int REC = paged_rec_floats(D);
+        float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
+        for (int i = tid; i < nrow * (D / 4); i += kThreads) {
+            const int row = i / (D / 4), c = 4 * (i % (D / 4));
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float2* rec = reinterpret_cast<const float2*>(mg + (w * ROWS + row) * (D + 2) + c);
+                const float f = fac[row * kWarps + w];
+                const float2 u = rec[0], v = rec[1];
+                o = make_float4(fmaf(u.x, f, o.x), fmaf(u.y, f, o.y), fmaf(v.x, f, o.z), fmaf(v.y, f, o.w));
             }
+            if (whole) store(row, c, ml[2 * row + 1], o);
+            else *reinterpret_cast<float4*>(part + row * D + c) = o;
+        }
+        if (tid < nrow) {
+            if (whole) store_lse(tid, ml[2 * tid], ml[2 * tid + 1]);
+            else *reinterpret_cast<float2*>(part + kRowsMax * D + 2 * tid) = make_float2(ml[2 * tid], ml[2 * tid + 1]);
         }
         if (!whole) {
-            // the last CTA of a split unit to get here merges its partials, in the order of the CTAs
+            // the last CTA of a split unit to get here merges its shares, in the order of the CTAs
             const long long tt = s_prefix[groups];
             const int lo = paged_tile_owner(s_seg[0] + kSeg, tt, GC), hi = paged_tile_owner(s_seg[1] - 1, tt, GC);
             __threadfence();
@@ -947,38 +971,48 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                 __threadfence();
                 const float* const base = p.partials + size_t(2 * lo + 1) * REC;   // slot of CTA lo, then 2k
                 const int n = hi - lo + 1;
-                float* const fac = mg;                     // [nrow][n]: factor of every partial; then M and L
-                float* const ml = mg + nrow * n;
+                float* const fs = mg;                      // [nrow][n]
                 auto slot = [&](int k) { return k == 0 ? base : base + size_t(2 * k - 1) * REC; };
                 for (int row = warp; row < nrow; row += kWarps) {
-                    float M = -INFINITY;
-                    for (int k = lane; k < n; k += 32) M = fmaxf(M, __ldcg(slot(k) + row * (D + 2) + D));
+                    float M = -INFINITY, L = 0.f;
+                    for (int k0 = 0; k0 < n; k0 += 32) {   // running (M, L) over 32 shares at a time
+                        const int k = k0 + lane;
+                        float2 v = make_float2(-INFINITY, 0.f);
+                        if (k < n) v = __ldcg(reinterpret_cast<const float2*>(slot(k) + kRowsMax * D + 2 * row));
+                        float m = v.x;
 #pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-                    float L = 0.f;
-                    for (int k = lane; k < n; k += 32) {
-                        const float m = __ldcg(slot(k) + row * (D + 2) + D);
-                        const float f = m == -INFINITY ? 0.f : ex2(m - M);
-                        fac[row * n + k] = f;
-                        L += f * __ldcg(slot(k) + row * (D + 2) + D + 1);
+                        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        m = fmaxf(m, M);
+                        float l = v.y * (v.x == -INFINITY ? 0.f : ex2(v.x - m));
+#pragma unroll
+                        for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                        L = (M == -INFINITY ? 0.f : L * ex2(M - m)) + l;
+                        M = m;
+                        if (k < n) fs[row * n + k] = v.x;
                     }
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+                    __syncwarp();
+                    for (int k = lane; k < n; k += 32) {
+                        const float m = fs[row * n + k];
+                        fs[row * n + k] = m == -INFINITY ? 0.f : ex2(m - M);
+                    }
                     if (lane == 0) {
-                        ml[2 * row] = M;
                         ml[2 * row + 1] = L;
+                        store_lse(row, M, L);
                     }
                 }
                 __syncthreads();
-                for (int i = tid; i < nrow * D; i += kThreads) {
-                    const int row = i / D, c = i % D;
-                    float O = 0.f;
+                for (int i = tid; i < nrow * (D / 4); i += kThreads) {
+                    const int row = i / (D / 4), c = 4 * (i % (D / 4));
+                    const float* const f = fs + row * n;
+                    const int at = row * D + c;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
                     for (int k = 0; k < n; ++k) {
-                        const float f = fac[row * n + k], o = __ldcg(slot(k) + row * (D + 2) + c);
-                        O += f * o;
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(k) + at));
+                        o = make_float4(fmaf(v.x, f[k], o.x), fmaf(v.y, f[k], o.y), fmaf(v.z, f[k], o.z),
+                                        fmaf(v.w, f[k], o.w));
                     }
-                    store(row, c, ml[2 * row], ml[2 * row + 1], O);
+                    store(row, c, ml[2 * row + 1], o);
                 }
             }
         }
@@ -992,11 +1026,11 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
 
 }  // namespace
 
-// Workspace after the header: [2 * SMs] arrival counters, then two partials of 16 rows for each CTA.
+// Workspace after the header: [2 * SMs] arrival counters, then two shares of 16 rows for each CTA.
 static size_t paged_attend_grid_max() { return size_t(device_info().num_sms) * 2; }
 size_t paged_attend_scratch_bytes(int d) {
     const size_t grid = paged_attend_grid_max();
-    return align_up(grid * 4, 256) + align_up(2 * grid * kRowsMax * (d + 2) * 4, 256);
+    return align_up(grid * 4, 256) + align_up(2 * grid * paged_rec_floats(d) * 4, 256);
 }
 void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch) {
     p.arrived = reinterpret_cast<int*>(scratch);
