@@ -557,11 +557,13 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
  *   spa_sparse_attend takes them: [U, cap] and [U], entry e covers tokens [e * unit_tokens,
  *   (e + 1) * unit_tokens) below kv_len[b]; U = B * Hkv (collapse GROUP_MEAN) or B * Hq (NONE).
  *   q [T, Hq, d] bf16 with token and head strides (elements, multiples of 8), 16-byte aligned;
- *   out [T, Hq, d] bf16, out_f32 [T, Hq, d] fp32 (optional), lse [T, Hq] fp32 (optional).
+ *   out [T, Hq, d] bf16, out_f32 [T, Hq, d] fp32 (optional), both 16-byte aligned as ws is;
+ *   lse [T, Hq] fp32 (optional).
  * A query that sees nothing gives out = 0 and lse = -inf.  Weights are carried in 11 bits (4-bit
  * cache: fp16 against exact codes) or about 16 (bf16 cache), sums in binary32.  What a
  * query does not see does not reach it, values that are not finite included.
- * Hq / Hkv <= 16; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(d). */
+ * Hq / Hkv <= 16; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(a);
+ * a workspace serves calls of the same arguments but for the pointers' values. */
 typedef struct spa_paged_attend_args {
     spa_paged_kv kv;
     int T, Hq;
@@ -578,7 +580,8 @@ typedef struct spa_paged_attend_args {
 } spa_paged_attend_args;
 
 spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_bytes, void* stream);
-size_t spa_paged_attend_workspace_bytes(int d);   /* depends on the current device's SM count */
+/* Depends on the arguments other than the pointers' values and on the current device's SM count. */
+size_t spa_paged_attend_workspace_bytes(const spa_paged_attend_args* a);
 
 /* ------------------------------------------------------------------------------------
  * Device status word of a workspace (sticky OR of SPA_ERR_* bits as (1 << code)).

@@ -682,7 +682,7 @@ def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     a.out, a.out_f32, a.lse = _ptr(out), _ptr(out32), _ptr(lse)
     plan = PagedAttendPlan(a, out, out32, lse, (q, cache, page_table, kv_len, seq_start, idx, count))
     with torch.cuda.device(dev):
-        plan._start(cache, "spa_paged_attend", ws, lib().spa_paged_attend_workspace_bytes(d),
+        plan._start(cache, "spa_paged_attend", ws, lib().spa_paged_attend_workspace_bytes(ctypes.byref(a)),
                     (out, out32, lse))
     if run:
         plan.run()

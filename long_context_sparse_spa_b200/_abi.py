@@ -150,7 +150,7 @@ SIGNATURES = {
     "spa_paged_append": (_i, [ctypes.POINTER(SpaPagedAppendArgs), _p, _sz, _p]),
     "spa_paged_gather": (_i, [ctypes.POINTER(SpaPagedGatherArgs), _p, _sz, _p]),
     "spa_paged_attend": (_i, [ctypes.POINTER(SpaPagedAttendArgs), _p, _sz, _p]),
-    "spa_paged_attend_workspace_bytes": (_sz, [_i]),
+    "spa_paged_attend_workspace_bytes": (_sz, [ctypes.POINTER(SpaPagedAttendArgs)]),
 }
 
 _LIB = None

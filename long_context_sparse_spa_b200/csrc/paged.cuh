@@ -48,6 +48,14 @@ struct PagedAttendParams {
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_attend_scratch_bytes(int d);
 void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch);   // the workspace after its header
+// paged_chunk.cu: more than 16 rows per sequence on average, 4-bit rows
+inline bool paged_chunk_taken(int format, const void* seq_start, const void* idx, int T, int Hq, int Hkv, int B,
+                              float sm_scale) {
+    return format == SPA_KV_INT4 && seq_start && !idx && sm_scale > 0.f && (long long)T * (Hq / Hkv) > 16ll * B;
+}
+spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st);
+size_t paged_chunk_scratch_bytes(int d);
+void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch);
 constexpr int kPagedMaxUnits = 512;   // sequences, or supports, of one launch: 4 bytes of shared memory each
 
 }  // namespace spa

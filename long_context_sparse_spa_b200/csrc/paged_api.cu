@@ -117,7 +117,15 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
     return launch_paged_gather(p, static_cast<cudaStream_t>(stream));
 }
 
-size_t spa_paged_attend_workspace_bytes(int d) { return d <= 0 ? 0 : kWsHeader + paged_attend_scratch_bytes(d); }
+static bool chunk_taken(const spa_paged_attend_args* a) {
+    return a->kv.Hkv > 0 && paged_chunk_taken(a->kv.format, a->seq_start, a->idx, a->T, a->Hq, a->kv.Hkv, a->kv.B,
+                                              a->sm_scale);
+}
+
+size_t spa_paged_attend_workspace_bytes(const spa_paged_attend_args* a) {
+    if (!a || a->kv.d <= 0) return 0;
+    return kWsHeader + (chunk_taken(a) ? paged_chunk_scratch_bytes(a->kv.d) : paged_attend_scratch_bytes(a->kv.d));
+}
 
 spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_bytes, void* stream) {
     if (!a) return SPA_ERR_INVALID_ARG;
@@ -132,11 +140,12 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     s = check_rows(a->q, a->q_token_stride, a->q_head_stride);
     if (s != SPA_OK) return s;
     if (a->Hq / a->kv.Hkv > 16) return SPA_ERR_UNSUPPORTED_SHAPE;
+    if (!aligned16(a->out) || !aligned16(a->out_f32) || !aligned16(ws)) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (a->idx) {
         if (a->seq_start || a->cap < 0 || a->unit_tokens <= 0) return SPA_ERR_INVALID_ARG;
         if (a->collapse != SPA_COLLAPSE_NONE && a->collapse != SPA_COLLAPSE_GROUP_MEAN) return SPA_ERR_INVALID_ARG;
     }
-    if (ws_bytes < spa_paged_attend_workspace_bytes(a->kv.d)) return SPA_ERR_WORKSPACE_TOO_SMALL;
+    if (ws_bytes < spa_paged_attend_workspace_bytes(a)) return SPA_ERR_WORKSPACE_TOO_SMALL;
     uint8_t* const w = static_cast<uint8_t*>(ws);
     p.T = a->T;
     p.Hq = a->Hq;
@@ -154,6 +163,10 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     p.out_f32 = a->out_f32;
     p.lse = a->lse;
     p.status = reinterpret_cast<uint32_t*>(w);
+    if (chunk_taken(a)) {
+        paged_chunk_carve(p, w + kWsHeader);
+        return launch_paged_chunk(p, static_cast<cudaStream_t>(stream));
+    }
     paged_attend_carve(p, w + kWsHeader);
     return launch_paged_attend(p, static_cast<cudaStream_t>(stream));
 }

@@ -1,0 +1,827 @@
+// Exact softmax attention of many new tokens per sequence over a 4-bit paged KV cache (a prefill chunk
+// against its cached prefix, drafted tokens of a large batch) on tcgen05 tensor cores.
+//
+// A unit is up to 256 (query token, head) rows that share one (sequence, kv head): two tiles of 128 rows.
+// Per 128 cached tokens and row tile:
+//   S = Q K^T        fp16 x fp16, fp32 in TMEM; K = scale * (code - 8) has at most 8 + 3 significant bits,
+//                    so it is exact in fp16 once a power of two per 64 tokens (per token where some queries
+//                    do not see all of them) brings the scales into range;
+//                    Q is scaled by a power of two per row (exact above 2^-24 of the row's largest channel)
+//   P = 2^(logit + log2(V's power of two) - reference) in fp16, at most 2^15, from registers to TMEM over S
+//   O += P V         P as the TMEM operand, V exact in fp16 like K; fp32 in TMEM
+// with the online softmax's reference per row following (logit + V's power of two); it moves, and O is
+// rescaled through TMEM, only when it is exceeded by 2^6.  l is summed in fp32.
+//
+// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row), 8-11 unpack the cache (8, 9 keys,
+// 10, 11 values; a thread is a token), 12 issues the MMAs.  While one row tile is in its softmax the
+// tensor cores work for the other.  Raw rows come by cp.async two steps of 64 tokens ahead; the unpacked
+// K and V tiles are double-buffered.  Each row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
+// order, so an observed S(t) also means that P(t-1) V is complete and O may be read and rescaled.
+//
+// Units are split evenly over the SMs by 128-token tiles as in paged_attend.cu; the last CTA of a split
+// unit merges its shares in the order of the CTAs.
+#include "paged.cuh"
+#include "tc.cuh"
+
+#include <cuda_fp16.h>
+
+namespace spa {
+namespace {
+
+using namespace tc;
+
+constexpr int kKeys = 128;                // tokens per tile
+constexpr int kHalf = 64;                 // tokens per unpacking step
+constexpr int kThreads = 13 * 32;
+constexpr int kSegC = 6;                  // tiles charged to a unit
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kBase = 9.f, kSlack = 6.f;
+constexpr uint32_t kSpin = 1u << 22;
+
+template <int D>
+struct ChunkShared {
+    static constexpr int kSlabs = D / 64;
+    static constexpr int kTile = kSlabs * kSlab;       // 128 rows of D fp16
+    static constexpr int ROWB = D + 16;
+    uint8_t q[2][kTile];
+    uint8_t k[2][kTile];
+    uint8_t v[2][kTile];
+    uint8_t raw[3][kHalf * ROWB];
+    long long rowoff[4][kHalf];                        // byte offset of a step's rows in the cache, -1: none
+    uint64_t s_full[2], p_full[2], k_full[2], v_full[2], k_empty[2], v_empty[2], o_done, q_full;
+    int ek[4][2], ev[4][2];                            // the powers of two of tile t (slot t % 4), by half
+    alignas(16) int8_t ek1[4][kKeys];                  // ... of a tile that not all queries see whole: by token
+    alignas(16) int8_t ev1[4][kKeys];
+    uint32_t poison[4][4][4];                          // tile t: tokens whose values of group g are not finite
+    uint32_t tmem_base;
+    int fail;                                          // a bounded wait gave up
+    int last;
+    alignas(16) uint32_t valid[4][4];                  // tile t: tokens that exist
+    long long wsum[16];
+};
+
+__device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t h2(float x) { return pack_f16(x, x); }
+__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ void arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc));
+}
+// Instruction descriptor of kind::f16 with fp16 A and B, fp32 D; B K- or MN-major
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+    return (1u << 4) | (uint32_t(b_mn_major) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};\n" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+// eight codes of a word, in the order 0 4 1 5 2 6 3 7, times the fp16 pairs s04, s15, ... (see the callers)
+__device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t sa, uint32_t sb) {
+    const uint32_t m8 = 0xe408e408u;                   // -1032
+    const uint32_t m72 = 0xd480d480u, sixteenth = 0x2c002c00u;   // -72
+    const uint32_t h = w >> 8;
+    const uint32_t c0 = add_f16x2((w & 0x000f000fu) | 0x64006400u, m8);                   // 1024 + u - 1032
+    const uint32_t c1 = fma_f16x2((w & 0x00f000f0u) | 0x64006400u, sixteenth, m72);       // (1024 + 16 u) / 16 - 72
+    const uint32_t c2 = add_f16x2((h & 0x000f000fu) | 0x64006400u, m8);
+    const uint32_t c3 = fma_f16x2((h & 0x00f000f0u) | 0x64006400u, sixteenth, m72);
+    return make_uint4(mul_f16x2(c0, sa), mul_f16x2(c1, sa), mul_f16x2(c2, sb), mul_f16x2(c3, sb));
+}
+
+// floats of one share of a split unit: O [D / 4][256][4], then m, l and the poisoned groups of each row
+__host__ __device__ constexpr int chunk_rec_floats(int d) { return 256 * (d + 3); }
+
+struct SeqG { int n, len, row0; };
+__device__ __forceinline__ SeqG seq_geo(const PagedAttendParams& p, int b, bool* bad) {
+    SeqG s;
+    s.len = paged_len(p.kv, p.kv.kv_len[b], bad);
+    const long long a = p.seq_start[b], e = p.seq_start[b + 1];
+    if (a < 0 || e > p.T || e < a) { *bad = true; s.n = 0; s.row0 = 0; }
+    else { s.n = int(e - a); s.row0 = int(a); }
+    return s;
+}
+__device__ __forceinline__ long long head_weight(const SeqG& s, int TQ) {
+    long long w = 0;
+    const int nj = (s.n + TQ - 1) / TQ;
+    for (int j = 0; j < nj; ++j) {
+        const int lim = paged_tile_limit(s.len, s.n, TQ, j);
+        if (lim > 0) w += (lim + kKeys - 1) / kKeys + kSegC;
+    }
+    return w;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
+    using SH = ChunkShared<D>;
+    static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && offsetof(SH, rowoff) % 8 == 0 &&
+                  sizeof(SH) % 8 == 0, "alignment of shared accesses");
+    constexpr int ROWB = SH::ROWB, WORDS = D / 8;      // 16-byte pieces of an operand row, code words of a row
+    extern __shared__ __align__(1024) uint8_t dyn[];
+    SH& sh = *reinterpret_cast<SH*>(dyn);
+    long long* const s_prefix = reinterpret_cast<long long*>(dyn + sizeof(SH));   // [groups + 1]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.Hq / p.kv.Hkv;
+
+    if (warp == 0) tmem_alloc(&sh.tmem_base, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.k_full[i], kKeys);
+            mbar_init(&sh.v_full[i], kKeys);
+            mbar_init(&sh.k_empty[i], 1);
+            mbar_init(&sh.v_empty[i], 1);
+        }
+        mbar_init(&sh.o_done, 1);
+        mbar_init(&sh.q_full, 256);
+        sh.fail = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    pdl_enter();
+
+    // ---- weighted tile prefix over the sequences
+    long long running = 0;
+    bool empties = false;
+    for (int base = 0; base < groups; base += kThreads) {
+        const int u = base + tid;
+        long long t = 0;
+        if (u < groups) {
+            bool bad = false;
+            const SeqG s = seq_geo(p, g0 + u, &bad);
+            t = head_weight(s, TQ) * p.kv.Hkv;
+            empties |= s.n > 0 && paged_tile_limit(s.len, s.n, TQ, 0) == 0;
+            if (bad && blockIdx.x == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+        }
+        long long incl = t;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += x;
+        }
+        if (lane == 31) sh.wsum[warp] = incl;
+        __syncthreads();
+        long long before = running, tot = 0;
+        for (int w = 0; w < kThreads / 32; ++w) {
+            if (w < warp) before += sh.wsum[w];
+            tot += sh.wsum[w];
+        }
+        if (u < groups) s_prefix[u] = before + incl - t;
+        running += tot;
+        __syncthreads();
+    }
+    if (tid == 0) s_prefix[groups] = running;
+    tc_fence_before();
+    empties = __syncthreads_or(empties);               // (also: barriers initialised, TMEM allocated)
+    tc_fence_after();
+    const long long TT = running;
+    const int cta = blockIdx.x;
+    const long long shares = (TT + kSegC) / (kSegC + 1);
+    const int GC = int(shares < (long long)gridDim.x ? shares : (long long)gridDim.x);
+    const uint32_t tmem = sh.tmem_base;
+
+    // ---- query tiles that see no key: out = 0, lse = -inf
+    for (int u = cta; empties && u < groups; u += gridDim.x) {
+        bool bad = false;
+        const SeqG s = seq_geo(p, g0 + u, &bad);
+        for (int j = 0; j * TQ < s.n && paged_tile_limit(s.len, s.n, TQ, j) == 0; ++j) {
+            const int rows = min(TQ, s.n - j * TQ) * p.Hq;
+            const size_t r0 = size_t(s.row0 + j * TQ) * p.Hq;
+            for (int i = tid; i < rows * D; i += kThreads) {
+                p.out[r0 * D + i] = 0;
+                if (p.out_f32) p.out_f32[r0 * D + i] = 0.f;
+                if (p.lse && i % D == 0) p.lse[r0 + i / D] = -INFINITY;
+            }
+        }
+    }
+
+    // bounded wait on a barrier's phase; on expiry, or once another thread's has expired, false
+    auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
+        for (uint32_t it = 0; !mbar_try_wait(bar, par); ++it) {
+            if (it >= kSpin || ((it & 255u) == 255u && *reinterpret_cast<volatile int*>(&sh.fail))) {
+                if (it >= kSpin) raise_status(p.status, SPA_ERR_TIMEOUT);
+                *reinterpret_cast<volatile int*>(&sh.fail) = 1;
+                return false;
+            }
+        }
+        return true;
+    };
+
+    const long long x0 = cta < GC ? TT * cta / GC : 0, x1 = cta < GC ? TT * (cta + 1) / GC : 0;
+    int grp = 0;
+    {
+        int lo = 0, hi = groups;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (s_prefix[mid] <= x0) lo = mid; else hi = mid;
+        }
+        grp = lo;
+    }
+    const float sl2 = p.sm_scale * kLog2e;
+    // uses of the barriers so far, by role: tiles filled / consumed over all segments, and segments
+    uint32_t tiles_done = 0, tiles1_done = 0, segs = 0;   // (tiles1: those in which row tile 1 took part)
+
+    long long x = x0;
+    while (x < x1) {
+        while (s_prefix[grp + 1] <= x) ++grp;
+        bool bad = false;
+        const SeqG sq = seq_geo(p, g0 + grp, &bad);
+        const long long hw = (s_prefix[grp + 1] - s_prefix[grp]) / p.kv.Hkv;
+        long long rem = x - s_prefix[grp];
+        const int g = int(rem / hw);
+        rem -= g * hw;
+        long long u_lo = s_prefix[grp] + g * hw;
+        int j = 0, lim;
+        for (;;) {
+            lim = paged_tile_limit(sq.len, sq.n, TQ, j);
+            const long long w = lim > 0 ? (lim + kKeys - 1) / kKeys + kSegC : 0;
+            if (rem < w) break;
+            rem -= w;
+            u_lo += w;
+            ++j;
+        }
+        const int nq = min(TQ, sq.n - j * TQ), nrow = nq * G, ntile = nrow > 128 ? 2 : 1;
+        const int lim0 = lim - nq + 1;                 // keys the first query token sees
+        const int row0 = sq.row0 + j * TQ;
+        const int tiles = (lim + kKeys - 1) / kKeys;
+        const long long u_hi = u_lo + kSegC + tiles;
+        const long long seg_end = x1 < u_hi ? x1 : u_hi;
+        const int a = int(x - u_lo) - kSegC > 0 ? int(x - u_lo) - kSegC : 0;
+        const int bnd = int(seg_end - u_lo) - kSegC > 0 ? int(seg_end - u_lo) - kSegC : 0;
+        if (a >= bnd) {
+            x = seg_end;
+            continue;
+        }
+        const int nt = bnd - a;
+        const uint32_t base = tiles_done;              // tile index of this segment's first tile, over the kernel
+        const uint32_t base1 = tiles1_done;
+        tiles_done += uint32_t(nt);
+        if (ntile == 2) tiles1_done += uint32_t(nt);
+
+        if (warp >= 8 && warp < 12) {
+            // ================================================================ unpacking
+            const int ut = tid - 256;                  // 0 .. 127
+            const bool isv = ut >= 64;
+            const int tok = ut & 63;
+            const int steps = 2 * nt;
+            // cache offset of token i of step h, or -1
+            auto page_of = [&](int h) -> int {
+                if (h >= steps || ut >= kHalf) return -1;
+                const long long n = (long long)a * kKeys + h * kHalf + ut;
+                if (n >= lim) return -1;
+                const long long s = paged_slot(p.kv, g0 + grp, n);
+                return s < 0 ? -1 : __ldg(p.kv.page_table + s);
+            };
+            auto put_rows = [&](int h, int pid) {
+                if (ut < kHalf) {
+                    const long long n = (long long)a * kKeys + h * kHalf + ut;
+                    long long off = -1;
+                    if (h < steps && n < lim) {
+                        off = paged_row(p.kv, pid, g, n);
+                        if (off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+                    }
+                    sh.rowoff[h & 3][ut] = off;
+                }
+            };
+            auto fetch = [&](int h) {                  // raw rows of step h; rows that do not exist become zero
+                if (h < steps) {
+                    constexpr int CPR = ROWB / 16;
+                    uint8_t* dst = sh.raw[h % 3];
+                    for (int i = ut; i < kHalf * CPR; i += 128) {
+                        const int r = i / CPR, c = i - r * CPR;
+                        const long long off = sh.rowoff[h & 3][r];
+                        cp_async16(smem_u32(dst + i * 16), p.kv.data + (off >= 0 ? off + c * 16 : 0), off >= 0);
+                    }
+                }
+                cp_async_commit();
+            };
+            auto sync = [&](bool v) -> bool {          // the 128 threads; the OR of v
+                uint32_t r;
+                asm volatile(
+                    "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, "
+                    "q;\n}\n"
+                    : "=r"(r)
+                    : "r"(uint32_t(v))
+                    : "memory");
+                return r != 0;
+            };
+            for (int h = 0; h < 3; ++h) put_rows(h, page_of(h));
+            int pid = page_of(3);
+            bool stop = sync(false);
+            fetch(0);
+            fetch(1);
+            for (int h = 0; h < steps; ++h) {
+                const uint32_t T = base + uint32_t(h >> 1);        // tile over the kernel
+                const int stage = T & 1, half = h & 1;
+                bool ok = true;
+                if (half == 0 && T >= 2)               // the tile two back has been read
+                    ok = wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1);
+                cp_async_wait_group<1>();
+                stop = sync(!ok);                      // raw(h) has landed; rows of step h + 2 are known
+                if (stop) break;
+                fetch(h + 2);
+                put_rows(h + 3, pid);
+                pid = page_of(h + 4);
+                const uint8_t* raw = sh.raw[h % 3];
+                // powers of two: the largest scale of the 64 tokens to [2^11, 2^12)
+                uint32_t kmx = 0, vmx = 0;
+                auto top = [](uint32_t w) -> uint32_t {   // larger of two bf16 that are numbers, its bits
+                    const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
+                    return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
+                };
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 s = *reinterpret_cast<const uint4*>(raw + (lane + 32 * i) * ROWB + D);
+                    kmx = max(kmx, max(top(s.x), top(s.y)));
+                    vmx = max(vmx, max(top(s.z), top(s.w)));
+                }
+                auto expo = [](uint32_t m) { return max(int(m >> 7) - 127, -70) - 11; };
+                const uint8_t* row = raw + tok * ROWB;
+                const uint4 all = *reinterpret_cast<const uint4*>(row + D);
+                // A tile that some queries do not see whole: every token has its own powers of two, so that what a
+                // query does not see cannot push what it sees out of fp16's range.
+                const bool edge = (a + (h >> 1) + 1) * kKeys > lim0;
+                int ek, ev;
+                if (edge) {
+                    ek = expo(max(top(all.x), top(all.y)));
+                    ev = expo(max(top(all.z), top(all.w)));
+                    if (!isv) {
+                        sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
+                        sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
+                    }
+                } else {
+                    ek = expo(__reduce_max_sync(0xffffffffu, kmx));
+                    ev = expo(__reduce_max_sync(0xffffffffu, vmx));
+                    if (ut == 0) {
+                        sh.ek[T & 3][half] = ek;
+                        sh.ev[T & 3][half] = ev;
+                    }
+                }
+                const uint2 sc = isv ? make_uint2(all.z, all.w) : make_uint2(all.x, all.y);
+                const float mul = pow2i(isv ? -ev : -ek);
+                float f[4] = {bf_lo(sc.x) * mul, bf_hi(sc.x) * mul, bf_lo(sc.y) * mul, bf_hi(sc.y) * mul};
+                const int r = half * kHalf + tok;      // row of the operand tile
+                if (isv) {
+                    // Tokens that some of the unit's queries do not see: a group that is not finite is taken as 0
+                    // (0 * NaN would reach every query) and noted for those that do see it.
+                    const int n = (a + (h >> 1)) * kKeys + r;
+#pragma unroll
+                    for (int gr = 0; gr < 4; ++gr) {
+                        const bool nan = edge && n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
+                        const uint32_t m = __ballot_sync(0xffffffffu, nan);
+                        if (lane == 0) sh.poison[T & 3][gr][r >> 5] = m;
+                        if (nan) f[gr] = 0.f;
+                    }
+                }
+                if (!isv) {
+                    const uint32_t m = __ballot_sync(0xffffffffu, sh.rowoff[h & 3][tok] >= 0);
+                    if (lane == 0) sh.valid[T & 3][r >> 5] = m;
+                }
+                uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
+                const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
+                // fp16 pairs of scales of a word's code pairs (0,4) (1,5) and (2,6) (3,7)
+                uint32_t s2[4][2];
+                if (D == 128) {
+                    if (isv) {                         // word (r, hh): groups 2 hh and 2 hh + 1
+                        s2[0][0] = s2[0][1] = pack_f16(f[0], f[1]);
+                        s2[1][0] = s2[1][1] = pack_f16(f[2], f[3]);
+                    } else {                           // word 4 t + g: group g
+#pragma unroll
+                        for (int gr = 0; gr < 4; ++gr) s2[gr][0] = s2[gr][1] = h2(f[gr]);
+                    }
+                } else {
+                    if (isv) {                         // word r: groups 0, 0, 1, 1 and 2, 2, 3, 3
+                        s2[0][0] = pack_f16(f[0], f[2]);
+                        s2[0][1] = pack_f16(f[1], f[3]);
+                    } else {                           // word 2 t + i: groups 2 i and 2 i + 1
+                        s2[0][0] = s2[0][1] = pack_f16(f[0], f[1]);
+                        s2[1][0] = s2[1][1] = pack_f16(f[2], f[3]);
+                    }
+                }
+#pragma unroll
+                for (int w4 = 0; w4 < WORDS / 4; ++w4) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + 4 * w4);
+                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int wi = 4 * w4 + i;
+                        uint4 o;
+                        if (isv) o = unpack8(ws[i], s2[D == 128 ? (i & 1) : 0][0], s2[D == 128 ? (i & 1) : 0][1]);
+                        else o = unpack8(ws[i], s2[D == 128 ? i : (i & 1)][0], s2[D == 128 ? i : (i & 1)][1]);
+                        // piece of the operand row: keys in word order; values so that a 64-channel slab is hh
+                        const int c = isv && D == 128 ? (wi & 1) * 8 + (wi >> 1) : wi;
+                        *reinterpret_cast<uint4*>(dst + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = o;
+                    }
+                }
+                fence_async_smem();
+                arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
+            }
+            cp_async_wait_group<0>();
+        } else if (warp == 12) {
+            // ================================================================ MMA issue
+            if (lane == 0) {
+                constexpr uint32_t kIdS = idesc_f16(128, kKeys, false);
+                constexpr uint32_t kIdO = idesc_f16(128, D, true);
+                auto s_mma = [&](int i, uint32_t T) {
+                    const uint64_t dq = sw128_desc(smem_u32(sh.q[i]), 16, 1024);
+                    const uint64_t dk = sw128_desc(smem_u32(sh.k[T & 1]), 16, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = uint64_t(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4);
+                        umma_bf16(tmem + i * 128, dq + off, dk + off, kIdS, kk > 0);
+                    }
+                    umma_commit(&sh.s_full[i]);
+                };
+                auto pv_mma = [&](int i, uint32_t T, bool first) {
+                    const uint64_t dv = sw128_desc(smem_u32(sh.v[T & 1]), kSlab, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kKeys / 16; ++kk)
+                        umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, dv + uint64_t((kk * 2048) >> 4), kIdO,
+                                (!first || kk > 0) ? 1u : 0u);
+                };
+                bool live = wait(&sh.q_full, segs & 1) && wait(&sh.k_full[base & 1], (base >> 1) & 1);
+                if (live) {
+                    tc_fence_after();
+                    for (int i = 0; i < ntile; ++i) s_mma(i, base);
+                    umma_commit(&sh.k_empty[base & 1]);
+                }
+                for (int t = 0; live && t < nt; ++t) {
+                    const uint32_t T = base + uint32_t(t);
+                    live = wait(&sh.v_full[T & 1], (T >> 1) & 1);
+                    if (live && t + 1 < nt) live = wait(&sh.k_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
+                    for (int i = 0; live && i < ntile; ++i) {
+                        live = wait(&sh.p_full[i], ((i ? base1 : base) + uint32_t(t)) & 1);
+                        if (!live) break;
+                        tc_fence_after();
+                        pv_mma(i, T, t == 0);
+                        if (i == ntile - 1) umma_commit(&sh.v_empty[T & 1]);
+                        if (t + 1 < nt) {
+                            s_mma(i, T + 1);
+                            if (i == ntile - 1) umma_commit(&sh.k_empty[(T + 1) & 1]);
+                        }
+                    }
+                }
+                umma_commit(&sh.o_done);
+                if (!live) wait(&sh.o_done, segs & 1);   // what was issued before a wait gave up
+            }
+            __syncwarp();
+        } else if (warp < 8) {
+            // ================================================================ softmax
+            const int rt = warp >> 2, r = (warp & 3) * 32 + lane, row = rt * 128 + r;
+            const bool have = row < nrow;
+            const uint32_t t_s = tmem + rt * 128 + (uint32_t((warp & 3) * 32) << 16);
+            const uint32_t t_o = t_s + 256;
+            const int lim_r = have ? lim0 + row / G : lim;
+            float hrow;
+            if (rt < ntile) {
+                // this row of Q: its largest channel to [2^13, 2^14), pieces and order as the keys'
+                const uint16_t* src = p.q + (have ? (row0 + row / G) * p.q_tok + (g * G + row % G) * p.q_head : 0);
+                uint4 w[WORDS];
+                uint32_t mx = 0;
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c) {
+                    w[c] = have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                    const uint32_t u4[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) mx = max(mx, max(u4[i] & 0x7fffu, (u4[i] >> 16) & 0x7fffu));
+                }
+                int ex = 13 - (int(mx >> 7) - 127);
+                ex = ex > 100 ? 100 : ex < -100 ? -100 : ex;
+                const float up = pow2i(ex);
+                hrow = sl2 * pow2i(-ex);
+                auto chan = [&](int ch) -> float {         // channel ch of the row, scaled
+                    const uint4 v = w[ch >> 3];
+                    const uint32_t u = (ch & 7) < 2 ? v.x : (ch & 7) < 4 ? v.y : (ch & 7) < 6 ? v.z : v.w;
+                    return (ch & 1 ? bf_hi(u) : bf_lo(u)) * up;
+                };
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c) {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {          // codes i and i + 4 of the key word c
+                        int c0, c1;
+                        if (D == 128) {
+                            c0 = 32 * (c & 3) + 8 * (c >> 2) + i;
+                            c1 = c0 + 4;
+                        } else {
+                            c0 = 16 * (2 * (c & 1)) + 4 * (c >> 1) + i;
+                            c1 = c0 + 16;
+                        }
+                        o[i] = pack_f16(chan(c0), chan(c1));
+                    }
+                    *reinterpret_cast<uint4*>(sh.q[rt] + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                }
+                fence_async_smem();
+            }
+            tc_fence_before();
+            arrive(&sh.q_full);
+
+            auto n0_of = [&](int t) { return (a + t) * kKeys; };
+            float m = -INFINITY, l = 0.f;
+            uint32_t nan = 0;                              // groups of V that are not finite in a token it sees
+            // values of tile t are unpacked once P(t) V is complete, which S(t + 1) shows
+            auto poisoned = [&](int t) {
+                if (n0_of(t) + kKeys <= lim0) return;
+                const int seen = lim_r - n0_of(t);
+#pragma unroll
+                for (int gr = 0; gr < 4; ++gr)
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int c = seen - 32 * w;
+                        const uint32_t vis = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
+                        if (sh.poison[(base + uint32_t(t)) & 3][gr][w] & vis) nan |= 1u << gr;
+                    }
+            };
+            bool ok = rt < ntile;
+            for (int t = 0; ok && t < nt; ++t) {
+                const uint32_t T = base + uint32_t(t), Ti = (rt ? base1 : base) + uint32_t(t);
+                ok = __all_sync(0xffffffffu, wait(&sh.s_full[rt], Ti & 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (t > 0) poisoned(t - 1);
+                const int n0 = n0_of(t);
+                const uint4 vd = *reinterpret_cast<const uint4*>(sh.valid[T & 3]);
+                const uint32_t vm[4] = {vd.x, vd.y, vd.z, vd.w};
+                const bool edge = n0 + kKeys > lim0, gaps = (vm[0] & vm[1] & vm[2] & vm[3]) != 0xffffffffu;
+                const int seen = lim_r - n0;               // columns below this one are seen
+                float cs[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
+                if (!edge) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        cs[h] = hrow * pow2i(sh.ek[T & 3][h]);
+                        ev[h] = float(sh.ev[T & 3][h]);
+                    }
+                }
+                // logits + V's power of two of 32 tokens, for tiles with tokens that are not seen or do not exist
+                auto masked = [&](int q4, float (&v)[32]) {
+#pragma unroll
+                    for (int i4 = 0; i4 < 8; ++i4) {
+                        const char4 e = reinterpret_cast<const char4*>(sh.ek1[T & 3])[q4 * 8 + i4];
+                        const char4 f = reinterpret_cast<const char4*>(sh.ev1[T & 3])[q4 * 8 + i4];
+                        const int ee[4] = {e.x, e.y, e.z, e.w}, ff[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int i = 4 * i4 + k;
+                            const float c = edge ? hrow * pow2i(ee[k]) : cs[q4 >> 1], o = edge ? float(ff[k]) : ev[q4 >> 1];
+                            v[i] = ((vm[q4] >> i) & 1u) && q4 * 32 + i < seen ? fmaf(v[i], c, o) : -INFINITY;
+                        }
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int q4 = 0; q4 < 4; ++q4) {
+                    float v[32];
+                    tmem_ld32(t_s + q4 * 32, v);
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    if (edge || gaps) masked(q4, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+                    const float x4 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    top = fmaxf(top, edge || gaps ? x4 : fmaf(x4, cs[q4 >> 1], ev[q4 >> 1]));
+                }
+                if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                    const float mn = top > m + kSlack ? top : m;
+                    const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
+                    m = mn;
+                    l *= f;
+                    if (t > 0) {                           // S(t) complete: so is P(t - 1) V
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            float v[32];
+                            tmem_ld32(t_o + c, v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] *= f;
+                            tmem_st32(t_o + c, v);
+                        }
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.f : kBase - m;
+                if (edge || gaps) {
+#pragma unroll 1
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        float v[32];
+                        tmem_ld32(t_s + q4 * 32, v);
+                        masked(q4, v);
+                        uint32_t o[16];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            v[i] = ex2_approx(v[i] + ref);
+                            const int e = edge ? sh.ev1[T & 3][q4 * 32 + i] : sh.ev[T & 3][q4 >> 1];
+                            l = fmaf(v[i], pow2i(-e), l);
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+                        tmem_st16(t_s + q4 * 16, o);
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float off = ev[h] + ref;
+                        float sum[2] = {0.f, 0.f};
+#pragma unroll
+                        for (int q2 = 0; q2 < 2; ++q2) {
+                            const int q4 = 2 * h + q2;
+                            float v[32];
+                            tmem_ld32(t_s + q4 * 32, v);
+                            uint32_t o[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                v[2 * i] = ex2_approx(fmaf(v[2 * i], cs[h], off));
+                                v[2 * i + 1] = ex2_approx(fmaf(v[2 * i + 1], cs[h], off));
+                                o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+                                sum[0] += v[2 * i];
+                                sum[1] += v[2 * i + 1];
+                            }
+                            tmem_st16(t_s + q4 * 16, o);
+                        }
+                        l = fmaf(sum[0] + sum[1], pow2i(-sh.ev[T & 3][h]), l);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(&sh.p_full[rt]);
+            }
+
+            // ---- output, or a share of a split unit
+            constexpr int REC = chunk_rec_floats(D);
+            const bool whole = a == 0 && bnd == tiles;
+            const bool in = rt < ntile;
+            ok = __all_sync(0xffffffffu, wait(&sh.o_done, segs & 1)) && ok;
+            tc_fence_after();
+            if (in && ok) poisoned(nt - 1);
+            // 64 channels of this row (column 64 hh + 8 r + q of O is channel 64 hh + r + perm(q))
+            auto put = [&](int hh, const float (&o)[64], float L) {
+                const float il = L == 0.f ? 0.f : 1.f / L;
+                const size_t at = (size_t(row0 + row / G) * p.Hq + g * G + row % G) * D + 64 * hh;
+                float y[64];
+#pragma unroll
+                for (int r8 = 0; r8 < 8; ++r8)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const int ch = r8 + ((q & 1) ? 32 : 0) + 8 * (q >> 1);
+                        const int gr = (64 * hh + ch) / (D / 4);
+                        y[ch] = (nan >> gr) & 1u ? __uint_as_float(0x7fc00000u) : o[8 * r8 + q] * il;
+                    }
+#pragma unroll
+                for (int c = 0; c < 64; c += 8) {
+                    uint32_t b[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(y[c + 2 * i], y[c + 2 * i + 1]);
+                        b[i] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    *reinterpret_cast<uint4*>(p.out + at + c) = make_uint4(b[0], b[1], b[2], b[3]);
+                    if (p.out_f32) {
+                        *reinterpret_cast<float4*>(p.out_f32 + at + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
+                        *reinterpret_cast<float4*>(p.out_f32 + at + c + 4) =
+                            make_float4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
+                    }
+                }
+                if (p.lse && hh == 0)
+                    p.lse[size_t(row0 + row / G) * p.Hq + g * G + row % G] =
+                        L == 0.f ? -INFINITY : (m - kBase + log2f(L)) * kLn2;
+            };
+            float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
+            if (in) {
+#pragma unroll
+                for (int hh = 0; hh < D / 64; ++hh) {
+                    float o[64], v[32];
+                    tmem_ld32(t_o + 64 * hh, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[i] = v[i];
+                    tmem_ld32(t_o + 64 * hh + 32, v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) o[32 + i] = v[i];
+                    if (whole) {
+                        if (have && ok) put(hh, o, l);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 64; c += 4)
+                            reinterpret_cast<float4*>(part)[(16 * hh + c / 4) * 256 + row] =
+                                make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+                if (!whole) {
+                    part[256 * D + row] = m;
+                    part[256 * D + 256 + row] = l;
+                    part[256 * D + 512 + row] = __uint_as_float(nan);
+                }
+            }
+            tc_fence_before();
+            if (!whole) {
+                const int lo = paged_tile_owner(u_lo + kSegC, TT, GC), hi = paged_tile_owner(u_hi - 1, TT, GC);
+                __threadfence();
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                if (tid == 0) {
+                    const int n = atomicAdd(p.arrived + lo, 1);
+                    sh.last = n == hi - lo;
+                    if (n == hi - lo) p.arrived[lo] = 0;
+                }
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                if (sh.last && have) {
+                    __threadfence();
+                    const float* const b0 = p.partials + size_t(2 * lo + 1) * REC;
+                    auto slot = [&](int k) { return k == 0 ? b0 : b0 + size_t(2 * k - 1) * REC; };
+                    const int n = hi - lo + 1;
+                    float M = -INFINITY, L = 0.f;
+                    for (int k = 0; k < n; ++k) M = fmaxf(M, __ldcg(slot(k) + 256 * D + row));
+                    for (int k = 0; k < n; ++k) {
+                        const float mk = __ldcg(slot(k) + 256 * D + row);
+                        L += (mk == -INFINITY ? 0.f : ex2_approx(mk - M)) * __ldcg(slot(k) + 256 * D + 256 + row);
+                    }
+                    m = M;
+                    for (int k = 0; k < n; ++k) nan |= __float_as_uint(__ldcg(slot(k) + 256 * D + 512 + row));
+#pragma unroll
+                    for (int hh = 0; hh < D / 64; ++hh) {
+                        float o[64];
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                        for (int k = 0; k < n; ++k) {
+                            const float mk = __ldcg(slot(k) + 256 * D + row);
+                            const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - M);
+#pragma unroll
+                            for (int c = 0; c < 64; c += 4) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(k)) + (16 * hh + c / 4) * 256 + row);
+                                o[c] = fmaf(v.x, f, o[c]);
+                                o[c + 1] = fmaf(v.y, f, o[c + 1]);
+                                o[c + 2] = fmaf(v.z, f, o[c + 2]);
+                                o[c + 3] = fmaf(v.w, f, o[c + 3]);
+                            }
+                        }
+                        put(hh, o, L);
+                    }
+                }
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            }
+        }
+        ++segs;
+        if (bad && tid == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+        x = seg_end;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+size_t paged_chunk_scratch_bytes(int d) {
+    const size_t grid = device_info().num_sms;
+    return align_up(grid * 4, 256) + align_up(2 * grid * chunk_rec_floats(d) * 4, 256);
+}
+void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch) {
+    p.arrived = reinterpret_cast<int*>(scratch);
+    p.partials = reinterpret_cast<float*>(scratch + align_up(size_t(device_info().num_sms) * 4, 256));
+}
+
+spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st) {
+    const int sms = device_info().num_sms;
+    const int TQ = paged_tokens_per_tile(256, p.Hq / p.kv.Hkv);
+    for (int g0 = 0; g0 < p.kv.B; g0 += kPagedMaxUnits) {
+        const int groups = p.kv.B - g0 < kPagedMaxUnits ? p.kv.B - g0 : kPagedMaxUnits;
+#define SPA_PC(DD)                                                                                              \
+    if (p.kv.d == DD) {                                                                                         \
+        constexpr size_t kMost = sizeof(ChunkShared<DD>) + size_t(kPagedMaxUnits + 1) * 8;                       \
+        static_assert(kMost <= 227 * 1024, "paged chunk: shared memory over the per-CTA limit");                 \
+        SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_chunk_kernel<DD>),                        \
+                                   cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)));                   \
+        SPA_CUDA_TRY(launch_pdl(paged_chunk_kernel<DD>, dim3(sms), dim3(kThreads),                               \
+                                sizeof(ChunkShared<DD>) + size_t(groups + 1) * 8, st, p, g0, groups, TQ));        \
+    }
+        SPA_PC(64) SPA_PC(128)
+#undef SPA_PC
+    }
+    return SPA_OK;
+}
+
+}  // namespace spa

@@ -328,6 +328,88 @@ def test_attend_several_queries_per_sequence(fmt, d, Hkv, G, page, new):
             check_attention(c, qv[t], out[t], lse[t], [sees] * Hkv, 0.11, b, f"sequence {b}, query {i}")
 
 
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+@pytest.mark.parametrize("d,Hkv,G,page,new,lens", [
+    (128, 2, 4, 64, [200, 3, 0, 64], [1500, 700, 90, 64]),      # several row tiles, a whole prompt, one short
+    (64, 1, 8, 16, [131], [131]),                               # a prompt from nothing
+    (128, 1, 1, 128, [300, 1], [2111, 1]),                      # one head: 256 tokens to a unit
+    (128, 3, 5, 16, [60, 52, 7], [60, 333, 4000]),              # rows that do not divide a tile
+    (64, 2, 16, 32, [33, 20], [500, 129])])
+def test_attend_a_chunk(fmt, d, Hkv, G, page, new, lens):
+    c = Cache(lens, Hkv, d, page, fmt, seed=d + G + 1)
+    start = np.concatenate(([0], np.cumsum(new)))
+    q = torch.randn(int(start[-1]), G * Hkv, d, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=1.5 * d**-0.5, seq_start=_i32(start), want_f32=True, **c.kw)
+    assert spa.read_device_status(plan.ws) == 0
+    out, lse, qv = _bf(plan.out), _np(plan.lse).astype(np.float64), _bf(q)
+    assert torch.equal(plan.out_f32.to(torch.bfloat16), plan.out)
+    rng = np.random.default_rng(G)
+    for b, (n, L) in enumerate(zip(new, lens)):
+        for i in sorted({0, 1, n // 2, n - 2, n - 1, *rng.integers(0, max(n, 1), 12)} & set(range(n))):
+            t = start[b] + i
+            check_attention(c, qv[t], out[t], lse[t], [np.arange(L) <= L - n + i] * Hkv, 1.5 * d**-0.5, b,
+                            f"sequence {b}, query {i}")
+    first = plan.out.clone()
+    plan.run()
+    assert torch.equal(first, plan.out)
+
+
+def test_a_long_chunk_is_split_and_merged():
+    c = Cache([30_000, 17], 1, 128, 64, INT4, seed=31)
+    start = [0, 90, 107]
+    q = (2 * torch.randn(107, 4, 128, device="cuda")).to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32(start), **c.kw)
+    out, lse, qv = _bf(plan.out), _np(plan.lse).astype(np.float64), _bf(q)
+    for t in (0, 1, 31, 32, 63, 64, 88, 89, 90, 106):
+        b, n = (0, 90) if t < 90 else (1, 17)
+        L = c.lens[b]
+        check_attention(c, qv[t], out[t], lse[t], [np.arange(L) <= L - n + t - start[b]], 0.1, b, f"row {t}")
+    first = plan.out.clone()
+    for _ in range(3):
+        plan.run()
+        assert torch.equal(first, plan.out)
+    assert spa.read_device_status(plan.ws) == 0
+
+
+@pytest.mark.parametrize("qs,ks,vs", [(1, 1, 1e-20), (1, 1, 1e30), (1e-20, 1e20, 1), (1e15, 1e-15, 1e-6), (40, 1, 1)])
+def test_chunk_scales_far_from_one(qs, ks, vs):
+    c = Cache([400], 1, 128, 16, INT4, seed=32, kscale=ks, vscale=vs)
+    q = (qs * torch.randn(60, 4, 128, device="cuda")).to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32([0, 60]), **c.kw)
+    for t in (0, 33, 59):
+        check_attention(c, _bf(q)[t], _bf(plan.out)[t], _np(plan.lse)[t].astype(np.float64), [np.arange(400) <= 340 + t],
+                        0.09, 0, f"row {t}")
+
+
+def test_chunk_masks_what_is_not_finite_and_bad_pages():
+    c = Cache([300], 1, 128, 16, INT4, seed=33)
+    host = c.pool.reshape(c.pool.shape[0], 1, 16, -1)
+    # token 260: its value's group 2 is NaN; token 290: its key; tokens 64-79: no page
+    host[c.table[0, 16], 0, 4, 128 + 12:128 + 14] = torch.tensor([0xC0, 0x7F], dtype=torch.uint8, device="cuda")
+    host[c.table[0, 18], 0, 2, 128:130] = torch.tensor([0xC0, 0x7F], dtype=torch.uint8, device="cuda")
+    c.kw["page_table"][0, 4] = -3
+    q = torch.randn(60, 4, 128, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32([0, 60]), **c.kw)
+    assert spa.read_device_status(plan.ws) == INVALID
+    out, lse, n = _bf(plan.out), _np(plan.lse).astype(np.float64), np.arange(300)
+    for t in (0, 10, 19, 20, 40, 49, 50, 59):
+        sees = (n <= 240 + t) & ((n < 64) | (n >= 80))
+        if t >= 50:
+            assert np.isnan(out[t]).all() and np.isnan(lse[t]).all()
+            continue
+        o = out[t].copy()
+        if t >= 20:
+            assert np.isnan(o[:, 64:96]).all()
+            o[:, 64:96] = 0
+            c.V[0][:, 260, 64:96] = 0
+            keep = c.V[0].copy()
+            c.V[0][:, :, 64:96] = 0
+            check_attention(c, _bf(q)[t], o, lse[t], [sees], 0.09, 0, f"row {t}")
+            c.V[0] = keep
+        else:
+            check_attention(c, _bf(q)[t], o, lse[t], [sees], 0.09, 0, f"row {t}")
+
+
 def test_queries_before_the_first_token_see_nothing():
     c = Cache([3], 1, 128, 16, INT4, seed=1)
     q = torch.randn(5, 4, 128, device="cuda").to(torch.bfloat16)

@@ -193,7 +193,7 @@ def test_small_workspaces_are_refused():
     g = _abi.SpaPagedGatherArgs(kv=_kv(), N=4, K=256, V=256)
     assert _call("spa_paged_gather", g, n=255) == "SPA_ERR_WORKSPACE_TOO_SMALL"
     t = _abi.SpaPagedAttendArgs(kv=_kv(), T=2, Hq=4, q=256, out=256)
-    need = _abi.lib().spa_paged_attend_workspace_bytes(128)
+    need = _abi.lib().spa_paged_attend_workspace_bytes(ctypes.byref(t))
     assert need > 256 and _call("spa_paged_attend", t, n=need - 1) == "SPA_ERR_WORKSPACE_TOO_SMALL"
     assert _call("spa_paged_attend", t, ws=None) == "SPA_ERR_INVALID_ARG"
 
@@ -201,6 +201,7 @@ def test_small_workspaces_are_refused():
 @pytest.mark.parametrize("kw,want", [
     (dict(Hq=5), "INVALID_ARG"), (dict(Hq=0), "INVALID_ARG"), (dict(Hq=34), "UNSUPPORTED_SHAPE"), (dict(T=3), "INVALID_ARG"),
     (dict(q=None), "INVALID_ARG"), (dict(out=None), "INVALID_ARG"), (dict(q=264), "UNSUPPORTED_SHAPE"),
+    (dict(out=264), "UNSUPPORTED_SHAPE"), (dict(out_f32=264), "UNSUPPORTED_SHAPE"),
     (dict(idx=256), "INVALID_ARG"), (dict(idx=256, count=256, unit_tokens=0), "INVALID_ARG"),
     (dict(idx=256, count=256, unit_tokens=1, cap=-1), "INVALID_ARG"),
     (dict(idx=256, count=256, unit_tokens=1, collapse=2), "INVALID_ARG"),
