@@ -12,8 +12,8 @@
 // with the online softmax's reference per row following (logit + V's power of two); it moves, and O is
 // rescaled through TMEM, only when it is exceeded by 2^6.  l is summed in fp32.
 //
-// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row), 8-11 unpack the cache (8, 9 keys,
-// 10, 11 values; a thread is a token), 12 issues the MMAs.  While one row tile is in its softmax the
+// Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row), 8-15 unpack the cache (8-11 keys,
+// 12-15 values; a thread has half of a token's codes), 16 issues the MMAs.  While one row tile is in its softmax the
 // tensor cores work for the other.  Raw rows come by cp.async two steps of 64 tokens ahead; the unpacked
 // K and V tiles are double-buffered.  Each row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
 // order, so an observed S(t) also means that P(t-1) V is complete and O may be read and rescaled.
@@ -32,7 +32,8 @@ using namespace tc;
 
 constexpr int kKeys = 128;                // tokens per tile
 constexpr int kHalf = 64;                 // tokens per unpacking step
-constexpr int kThreads = 13 * 32;
+constexpr int kUnpack = 8;                // unpacking warps
+constexpr int kThreads = (8 + kUnpack + 1) * 32;
 constexpr int kSegC = 6;                  // tiles charged to a unit
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -68,12 +69,6 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t h2(float x) { return pack_f16(x, x); }
-__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
-    uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
@@ -106,16 +101,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
-// eight codes of a word, in the order 0 4 1 5 2 6 3 7, times the fp16 pairs s04, s15, ... (see the callers)
-__device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t sa, uint32_t sb) {
-    const uint32_t m8 = 0xe408e408u;                   // -1032
-    const uint32_t m72 = 0xd480d480u, sixteenth = 0x2c002c00u;   // -72
-    const uint32_t h = w >> 8;
-    const uint32_t c0 = add_f16x2((w & 0x000f000fu) | 0x64006400u, m8);                   // 1024 + u - 1032
-    const uint32_t c1 = fma_f16x2((w & 0x00f000f0u) | 0x64006400u, sixteenth, m72);       // (1024 + 16 u) / 16 - 72
-    const uint32_t c2 = add_f16x2((h & 0x000f000fu) | 0x64006400u, m8);
-    const uint32_t c3 = fma_f16x2((h & 0x00f000f0u) | 0x64006400u, sixteenth, m72);
-    return make_uint4(mul_f16x2(c0, sa), mul_f16x2(c1, sa), mul_f16x2(c2, sb), mul_f16x2(c3, sb));
+// Fp16 pairs of scales s, and -8 s in the units of the two kinds of codes below.
+struct Scale2 {
+    uint32_t s, lo, hi;
+};
+__device__ __forceinline__ Scale2 scale2(float a, float b) {
+    Scale2 r;
+    r.s = pack_f16(a, b);
+    r.lo = mul_f16x2(r.s, 0x80408040u);                // -8 * 2^-21
+    r.hi = mul_f16x2(r.s, 0x84008400u);                // -8 * 2^-17
+    return r;
+}
+// Eight codes of a word as (u - 8) s, in the order 0 4 1 5 2 6 3 7.  A code in bits 3-6 is the fp16
+// denormal u * 2^-21, in bits 7-10 u * 2^-17 (bit 10 is the exponent's lowest, whose step is the denormals'):
+// even codes come times 2^-21, odd ones times 2^-17.  (u - 8) s has at most 3 + 8 bits, so with s up to 2^16
+// the result is exact for scales down to 2^-9 of that, and below within 2^-23 of the largest value.
+__device__ __forceinline__ uint4 unpack8(uint32_t w, const Scale2& a, const Scale2& b) {
+    const uint32_t x = w << 3, y = w >> 5;
+    return make_uint4(fma_f16x2(x & 0x00780078u, a.s, a.lo), fma_f16x2(x & 0x07800780u, a.s, a.hi),
+                      fma_f16x2(y & 0x00780078u, b.s, b.lo), fma_f16x2(y & 0x07800780u, b.s, b.hi));
 }
 
 // floats of one share of a split unit: O [D / 4][256][4], then m, l and the poisoned groups of each row
@@ -157,8 +161,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
             mbar_init(&sh.p_full[i], 128);
-            mbar_init(&sh.k_full[i], kKeys);
-            mbar_init(&sh.v_full[i], kKeys);
+            mbar_init(&sh.k_full[i], kUnpack);         // 4 warps x 2 steps
+            mbar_init(&sh.v_full[i], kUnpack);
             mbar_init(&sh.k_empty[i], 1);
             mbar_init(&sh.v_empty[i], 1);
         }
@@ -287,11 +291,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         tiles_done += uint32_t(nt);
         if (ntile == 2) tiles1_done += uint32_t(nt);
 
-        if (warp >= 8 && warp < 12) {
+        if (warp >= 8 && warp < 8 + kUnpack) {
             // ================================================================ unpacking
-            const int ut = tid - 256;                  // 0 .. 127
-            const bool isv = ut >= 64;
-            const int tok = ut & 63;
+            const int ut = tid - 256, uw = ut >> 5;    // 0 .. 255
+            const bool isv = uw >= 4;
+            const int part = (uw >> 1) & 1, tok = (uw & 1) * 32 + lane;
+            // 16-byte pieces of a step's rows that this thread copies: row, piece
+            constexpr int CPR = ROWB / 16, NCP = (kHalf * CPR + 255) / 256;
+            int cr[NCP], cpc[NCP];
+#pragma unroll
+            for (int i = 0; i < NCP; ++i) {
+                cr[i] = (ut + 256 * i) / CPR;
+                cpc[i] = (ut + 256 * i) % CPR;
+            }
             const int steps = 2 * nt;
             // cache offset of token i of step h, or -1
             auto page_of = [&](int h) -> int {
@@ -314,20 +326,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             };
             auto fetch = [&](int h) {                  // raw rows of step h; rows that do not exist become zero
                 if (h < steps) {
-                    constexpr int CPR = ROWB / 16;
                     uint8_t* dst = sh.raw[h % 3];
-                    for (int i = ut; i < kHalf * CPR; i += 128) {
-                        const int r = i / CPR, c = i - r * CPR;
-                        const long long off = sh.rowoff[h & 3][r];
-                        cp_async16(smem_u32(dst + i * 16), p.kv.data + (off >= 0 ? off + c * 16 : 0), off >= 0);
-                    }
+#pragma unroll
+                    for (int i = 0; i < NCP; ++i)
+                        if (cr[i] < kHalf) {
+                            const long long off = sh.rowoff[h & 3][cr[i]];
+                            cp_async16(smem_u32(dst + (ut + 256 * i) * 16), p.kv.data + (off >= 0 ? off + cpc[i] * 16 : 0),
+                                       off >= 0);
+                        }
                 }
                 cp_async_commit();
             };
-            auto sync = [&](bool v) -> bool {          // the 128 threads; the OR of v
+            auto sync = [&](bool v) -> bool {          // the 256 threads; the OR of v
                 uint32_t r;
                 asm volatile(
-                    "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 128, p;\n selp.u32 %0, 1, 0, "
+                    "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 256, p;\n selp.u32 %0, 1, 0, "
                     "q;\n}\n"
                     : "=r"(r)
                     : "r"(uint32_t(v))
@@ -352,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 put_rows(h + 3, pid);
                 pid = page_of(h + 4);
                 const uint8_t* raw = sh.raw[h % 3];
-                // powers of two: the largest scale of the 64 tokens to [2^11, 2^12)
+                // powers of two: the largest scale of the 64 tokens to [2^15, 2^16)
                 uint32_t kmx = 0, vmx = 0;
                 auto top = [](uint32_t w) -> uint32_t {   // larger of two bf16 that are numbers, its bits
                     const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
@@ -364,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                     kmx = max(kmx, max(top(s.x), top(s.y)));
                     vmx = max(vmx, max(top(s.z), top(s.w)));
                 }
-                auto expo = [](uint32_t m) { return max(int(m >> 7) - 127, -70) - 11; };
+                auto expo = [](uint32_t m) { return max(int(m >> 7) - 127, -70) - 15; };
                 const uint8_t* row = raw + tok * ROWB;
                 const uint4 all = *reinterpret_cast<const uint4*>(row + D);
                 // A tile that some queries do not see whole: every token has its own powers of two, so that what a
@@ -374,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 if (edge) {
                     ek = expo(max(top(all.x), top(all.y)));
                     ev = expo(max(top(all.z), top(all.w)));
-                    if (!isv) {
+                    if (uw < 2) {
                         sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
                         sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
                     }
@@ -398,55 +411,63 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                     for (int gr = 0; gr < 4; ++gr) {
                         const bool nan = edge && n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
                         const uint32_t m = __ballot_sync(0xffffffffu, nan);
-                        if (lane == 0) sh.poison[T & 3][gr][r >> 5] = m;
+                        if (lane == 0 && part == 0) sh.poison[T & 3][gr][r >> 5] = m;
                         if (nan) f[gr] = 0.f;
                     }
                 }
-                if (!isv) {
+                if (uw < 2) {
                     const uint32_t m = __ballot_sync(0xffffffffu, sh.rowoff[h & 3][tok] >= 0);
                     if (lane == 0) sh.valid[T & 3][r >> 5] = m;
                 }
                 uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
                 const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
-                // fp16 pairs of scales of a word's code pairs (0,4) (1,5) and (2,6) (3,7)
-                uint32_t s2[4][2];
+                // scale pairs of a word's code pairs (0,4) (1,5) and (2,6) (3,7), for the words that differ in them
+                Scale2 s2[4];
                 if (D == 128) {
-                    if (isv) {                         // word (r, hh): groups 2 hh and 2 hh + 1
-                        s2[0][0] = s2[0][1] = pack_f16(f[0], f[1]);
-                        s2[1][0] = s2[1][1] = pack_f16(f[2], f[3]);
+                    if (isv) {                         // word 2 r + hh: groups 2 hh and 2 hh + 1
+                        s2[0] = s2[2] = scale2(f[0], f[1]);
+                        s2[1] = s2[3] = scale2(f[2], f[3]);
                     } else {                           // word 4 t + g: group g
 #pragma unroll
-                        for (int gr = 0; gr < 4; ++gr) s2[gr][0] = s2[gr][1] = h2(f[gr]);
+                        for (int gr = 0; gr < 4; ++gr) s2[gr] = scale2(f[gr], f[gr]);
                     }
                 } else {
-                    if (isv) {                         // word r: groups 0, 0, 1, 1 and 2, 2, 3, 3
-                        s2[0][0] = pack_f16(f[0], f[2]);
-                        s2[0][1] = pack_f16(f[1], f[3]);
+                    if (isv) {                         // word r: groups 0 and 2, then 1 and 3
+                        s2[0] = scale2(f[0], f[2]);
+                        s2[1] = scale2(f[1], f[3]);
                     } else {                           // word 2 t + i: groups 2 i and 2 i + 1
-                        s2[0][0] = s2[0][1] = pack_f16(f[0], f[1]);
-                        s2[1][0] = s2[1][1] = pack_f16(f[2], f[3]);
+                        s2[0] = scale2(f[0], f[1]);
+                        s2[1] = scale2(f[2], f[3]);
                     }
                 }
+                // piece of the operand row: keys in word order; values so that a 64-channel slab is hh
+                uint8_t* const out = dst + r * 128;
 #pragma unroll
-                for (int w4 = 0; w4 < WORDS / 4; ++w4) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + 4 * w4);
+                for (int w4 = 0; w4 < WORDS / 8; ++w4) {
+                    const int at = part * (WORDS / 8) + w4;
+                    const uint4 w = *reinterpret_cast<const uint4*>(codes + 4 * at);
                     const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const int wi = 4 * w4 + i;
+                        const int wi = 4 * at + i;
                         uint4 o;
-                        if (isv) o = unpack8(ws[i], s2[D == 128 ? (i & 1) : 0][0], s2[D == 128 ? (i & 1) : 0][1]);
-                        else o = unpack8(ws[i], s2[D == 128 ? i : (i & 1)][0], s2[D == 128 ? i : (i & 1)][1]);
-                        // piece of the operand row: keys in word order; values so that a 64-channel slab is hh
-                        const int c = isv && D == 128 ? (wi & 1) * 8 + (wi >> 1) : wi;
-                        *reinterpret_cast<uint4*>(dst + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = o;
+                        int c;
+                        if constexpr (D == 128) {
+                            o = unpack8(ws[i], s2[i], s2[i]);
+                            c = isv ? (i & 1) * 8 + (wi >> 1) : wi;
+                        } else {
+                            o = isv ? unpack8(ws[i], s2[0], s2[1]) : unpack8(ws[i], s2[i & 1], s2[i & 1]);
+                            c = wi;
+                        }
+                        *reinterpret_cast<uint4*>(out + (c >> 3) * kSlab + (((c & 7) ^ (r & 7)) << 4)) = o;
                     }
                 }
                 fence_async_smem();
-                arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
+                __syncwarp();
+                if (lane == 0) arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
             }
             cp_async_wait_group<0>();
-        } else if (warp == 12) {
+        } else if (warp == 8 + kUnpack) {
             // ================================================================ MMA issue
             if (lane == 0) {
                 constexpr uint32_t kIdS = idesc_f16(128, kKeys, false);
@@ -517,7 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 int ex = 13 - (int(mx >> 7) - 127);
                 ex = ex > 100 ? 100 : ex < -100 ? -100 : ex;
                 const float up = pow2i(ex);
-                hrow = sl2 * pow2i(-ex);
+                hrow = sl2 * pow2i(-ex) * 2097152.f;       // 2^21: the unit of the even codes
                 auto chan = [&](int ch) -> float {         // channel ch of the row, scaled
                     const uint4 v = w[ch >> 3];
                     const uint32_t u = (ch & 7) < 2 ? v.x : (ch & 7) < 4 ? v.y : (ch & 7) < 6 ? v.z : v.w;
@@ -536,7 +557,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                             c0 = 16 * (2 * (c & 1)) + 4 * (c >> 1) + i;
                             c1 = c0 + 16;
                         }
-                        o[i] = pack_f16(chan(c0), chan(c1));
+                        // odd codes are held 2^4 times the even ones
+                        o[i] = (i & 1) ? pack_f16(chan(c0) * 0.0625f, chan(c1) * 0.0625f) : pack_f16(chan(c0), chan(c1));
                     }
                     *reinterpret_cast<uint4*>(sh.q[rt] + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
                         make_uint4(o[0], o[1], o[2], o[3]);
@@ -679,55 +701,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             ok = __all_sync(0xffffffffu, wait(&sh.o_done, segs & 1)) && ok;
             tc_fence_after();
             if (in && ok) poisoned(nt - 1);
-            // 64 channels of this row (column 64 hh + 8 r + q of O is channel 64 hh + r + perm(q))
-            auto put = [&](int hh, const float (&o)[64], float L) {
-                const float il = L == 0.f ? 0.f : 1.f / L;
-                const size_t at = (size_t(row0 + row / G) * p.Hq + g * G + row % G) * D + 64 * hh;
-                float y[64];
+            // 32 columns of this row: column 64 hh + 8 r + q of O is channel 64 hh + r + 32 (q % 2) + 8 (q / 2), held
+            // times 2^-21, or 2^-17 where its code is odd (q / 2 odd)
+            auto put = [&](int n, const float (&o)[32], float L) {
+                const float il = (L == 0.f ? 0.f : 1.f / L) * 2097152.f;
+                const int hh = n >> 6, r8 = (n & 63) >> 3;             // four r from r8 on
+                const size_t at = (size_t(row0 + row / G) * p.Hq + g * G + row % G) * D;
 #pragma unroll
-                for (int r8 = 0; r8 < 8; ++r8)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const int ch = r8 + ((q & 1) ? 32 : 0) + 8 * (q >> 1);
-                        const int gr = (64 * hh + ch) / (D / 4);
-                        y[ch] = (nan >> gr) & 1u ? __uint_as_float(0x7fc00000u) : o[8 * r8 + q] * il;
-                    }
-#pragma unroll
-                for (int c = 0; c < 64; c += 8) {
-                    uint32_t b[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(y[c + 2 * i], y[c + 2 * i + 1]);
-                        b[i] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    *reinterpret_cast<uint4*>(p.out + at + c) = make_uint4(b[0], b[1], b[2], b[3]);
-                    if (p.out_f32) {
-                        *reinterpret_cast<float4*>(p.out_f32 + at + c) = make_float4(y[c], y[c + 1], y[c + 2], y[c + 3]);
-                        *reinterpret_cast<float4*>(p.out_f32 + at + c + 4) =
-                            make_float4(y[c + 4], y[c + 5], y[c + 6], y[c + 7]);
-                    }
+                for (int q = 0; q < 8; ++q) {
+                    const int ch = 64 * hh + r8 + 32 * (q & 1) + 8 * (q >> 1);
+                    const bool bad = (nan >> (ch / (D / 4))) & 1u;
+                    const float f = bad ? __uint_as_float(0x7fc00000u) : (q >> 1) & 1 ? il * 0.0625f : il;
+                    const float4 y = make_float4(o[q] * f, o[8 + q] * f, o[16 + q] * f, o[24 + q] * f);
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+                    *reinterpret_cast<uint2*>(p.out + at + ch) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + at + ch) = y;
                 }
-                if (p.lse && hh == 0)
+                if (p.lse && n == 0)
                     p.lse[size_t(row0 + row / G) * p.Hq + g * G + row % G] =
                         L == 0.f ? -INFINITY : (m - kBase + log2f(L)) * kLn2;
             };
             float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
             if (in) {
-#pragma unroll
-                for (int hh = 0; hh < D / 64; ++hh) {
-                    float o[64], v[32];
-                    tmem_ld32(t_o + 64 * hh, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = v[i];
-                    tmem_ld32(t_o + 64 * hh + 32, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[32 + i] = v[i];
+#pragma unroll 1
+                for (int n = 0; n < D; n += 32) {
+                    float o[32];
+                    tmem_ld32(t_o + n, o);
                     if (whole) {
-                        if (have && ok) put(hh, o, l);
+                        if (have && ok) put(n, o, l);
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 64; c += 4)
-                            reinterpret_cast<float4*>(part)[(16 * hh + c / 4) * 256 + row] =
+                        for (int c = 0; c < 32; c += 4)
+                            reinterpret_cast<float4*>(part)[((n + c) / 4) * 256 + row] =
                                 make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                     }
                 }
@@ -761,24 +767,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                     }
                     m = M;
                     for (int k = 0; k < n; ++k) nan |= __float_as_uint(__ldcg(slot(k) + 256 * D + 512 + row));
+#pragma unroll 1
+                    for (int nn = 0; nn < D; nn += 32) {
+                        float o[32];
 #pragma unroll
-                    for (int hh = 0; hh < D / 64; ++hh) {
-                        float o[64];
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                        for (int i = 0; i < 32; ++i) o[i] = 0.f;
                         for (int k = 0; k < n; ++k) {
                             const float mk = __ldcg(slot(k) + 256 * D + row);
                             const float f = mk == -INFINITY ? 0.f : ex2_approx(mk - M);
 #pragma unroll
-                            for (int c = 0; c < 64; c += 4) {
-                                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(k)) + (16 * hh + c / 4) * 256 + row);
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 v = __ldcg(reinterpret_cast<const float4*>(slot(k)) + ((nn + c) / 4) * 256 + row);
                                 o[c] = fmaf(v.x, f, o[c]);
                                 o[c + 1] = fmaf(v.y, f, o[c + 1]);
                                 o[c + 2] = fmaf(v.z, f, o[c + 2]);
                                 o[c + 3] = fmaf(v.w, f, o[c + 3]);
                             }
                         }
-                        put(hh, o, L);
+                        put(nn, o, L);
                     }
                 }
                 asm volatile("bar.sync 1, 256;\n" ::: "memory");
