@@ -349,15 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             };
             for (int h = 0; h < 3; ++h) put_rows(h, page_of(h));
             int pid = page_of(3);
-            bool stop = sync(false);
+            bool stop = sync(false), ok = true;
             fetch(0);
             fetch(1);
             for (int h = 0; h < steps; ++h) {
                 const uint32_t T = base + uint32_t(h >> 1);        // tile over the kernel
                 const int stage = T & 1, half = h & 1;
-                bool ok = true;
-                if (half == 0 && T >= 2)               // the tile two back has been read
-                    ok = wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1);
                 cp_async_wait_group<1>();
                 stop = sync(!ok);                      // raw(h) has landed; rows of step h + 2 are known
                 if (stop) break;
@@ -418,6 +415,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 if (uw < 2) {
                     const uint32_t m = __ballot_sync(0xffffffffu, sh.rowoff[h & 3][tok] >= 0);
                     if (lane == 0) sh.valid[T & 3][r >> 5] = m;
+                }
+                if (half == 0 && T >= 2) {             // the tile two back has been read
+                    ok = __all_sync(0xffffffffu,
+                                    wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1));
+                    if (!ok) continue;                 // (all leave at the next step's barrier)
                 }
                 uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
                 const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
@@ -498,7 +500,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 for (int t = 0; live && t < nt; ++t) {
                     const uint32_t T = base + uint32_t(t);
                     live = wait(&sh.v_full[T & 1], (T >> 1) & 1);
-                    if (live && t + 1 < nt) live = wait(&sh.k_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
                     for (int i = 0; live && i < ntile; ++i) {
                         live = wait(&sh.p_full[i], ((i ? base1 : base) + uint32_t(t)) & 1);
                         if (!live) break;
@@ -506,6 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         pv_mma(i, T, t == 0);
                         if (i == ntile - 1) umma_commit(&sh.v_empty[T & 1]);
                         if (t + 1 < nt) {
+                            if (i == 0) live = wait(&sh.k_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
+                            if (!live) break;
+                            tc_fence_after();
                             s_mma(i, T + 1);
                             if (i == ntile - 1) umma_commit(&sh.k_empty[(T + 1) & 1]);
                         }
