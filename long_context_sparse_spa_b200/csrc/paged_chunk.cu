@@ -618,13 +618,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int i = 4 * i4 + k;
-                            const float c = edge ? hrow * pow2i(ee[k]) : cs[q4 >> 1], o = edge ? float(ff[k]) : ev[q4 >> 1];
+                            const float c = edge ? hrow * pow2i(ee[k]) : q4 < 2 ? cs[0] : cs[1];
+                            const float o = edge ? float(ff[k]) : q4 < 2 ? ev[0] : ev[1];
                             v[i] = ((vm[q4] >> i) & 1u) && q4 * 32 + i < seen ? fmaf(v[i], c, o) : -INFINITY;
                         }
                     }
                 };
+                // (the loops over 32 columns are not unrolled: the warps' roles share the instruction cache)
                 float top = -INFINITY;
-#pragma unroll
+#pragma unroll 1
                 for (int q4 = 0; q4 < 4; ++q4) {
                     float v[32];
                     tmem_ld32(t_s + q4 * 32, v);
@@ -633,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 #pragma unroll
                     for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
                     const float x4 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    top = fmaxf(top, edge || gaps ? x4 : fmaf(x4, cs[q4 >> 1], ev[q4 >> 1]));
+                    top = fmaxf(top, edge || gaps ? x4 : fmaf(x4, q4 < 2 ? cs[0] : cs[1], q4 < 2 ? ev[0] : ev[1]));
                 }
                 if (__any_sync(0xffffffffu, top > m + kSlack)) {
                     const float mn = top > m + kSlack ? top : m;
@@ -670,27 +672,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         tmem_st16(t_s + q4 * 16, o);
                     }
                 } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float off = ev[h] + ref;
+#pragma unroll 1
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        const float c = q4 < 2 ? cs[0] : cs[1], e = q4 < 2 ? ev[0] : ev[1], off = e + ref;
                         float sum[2] = {0.f, 0.f};
+                        float v[32];
+                        tmem_ld32(t_s + q4 * 32, v);
+                        uint32_t o[16];
 #pragma unroll
-                        for (int q2 = 0; q2 < 2; ++q2) {
-                            const int q4 = 2 * h + q2;
-                            float v[32];
-                            tmem_ld32(t_s + q4 * 32, v);
-                            uint32_t o[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                v[2 * i] = ex2_approx(fmaf(v[2 * i], cs[h], off));
-                                v[2 * i + 1] = ex2_approx(fmaf(v[2 * i + 1], cs[h], off));
-                                o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-                                sum[0] += v[2 * i];
-                                sum[1] += v[2 * i + 1];
-                            }
-                            tmem_st16(t_s + q4 * 16, o);
+                        for (int i = 0; i < 16; ++i) {
+                            v[2 * i] = ex2_approx(fmaf(v[2 * i], c, off));
+                            v[2 * i + 1] = ex2_approx(fmaf(v[2 * i + 1], c, off));
+                            o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
+                            sum[0] += v[2 * i];
+                            sum[1] += v[2 * i + 1];
                         }
-                        l = fmaf(sum[0] + sum[1], pow2i(-sh.ev[T & 3][h]), l);
+                        tmem_st16(t_s + q4 * 16, o);
+                        l = fmaf(sum[0] + sum[1], ex2_approx(-e), l);
                     }
                 }
                 tmem_wait_st();
