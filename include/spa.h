@@ -488,7 +488,7 @@ spa_status spa_pbs_prefill_timed(const spa_pbs_args* a, void* ws, size_t ws_byte
  * [B, max_pages] and kv_len [B] are int32 in device memory, read when the kernels run.
  * seq_start [B + 1] int32, device memory: the new tokens (rows of q, k, v, out) of sequence b
  * are rows [seq_start[b], seq_start[b + 1]), the last of them token kv_len[b] - 1; rows before
- * seq_start[0] or from seq_start[B] on belong to nobody: they are not read, and what they
+ * seq_start[0] or from seq_start[B] on belong to nobody: they have no effect, and what they
  * would be written to stays as it is.  NULL: one new token per sequence, T = B.
  * Device-side conditions raise (1 << SPA_ERR_INVALID_ARG) in the status word at the head of
  * ws: a page number outside [0, num_pages), a length outside [0, max_pages * page], a sequence

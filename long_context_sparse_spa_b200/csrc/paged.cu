@@ -22,12 +22,28 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kAppTok = 4;   // tokens per CTA: 4 x 64 angles are one per thread at d = 128
+constexpr int kAppAhead = 3; // passes whose loads are in flight
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+__device__ __forceinline__ float f4(const float4& v, int j) { return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// sin and cos of an angle of up to about 2^31 in fp64: the nearest multiple of pi/2 is taken off in two parts
+// with fused multiply-adds (Cody and Waite, "Software Manual for the Elementary Functions", 1980), so the
+// functions see |r| <= pi/4 whatever the position is.
+__device__ __forceinline__ void angle_sincos(double a, double* sn, double* cs) {
+    const double k = rint(a * 0.63661977236758134);
+    const double r = fma(-k, 6.123233995736766e-17, fma(-k, 1.5707963267948966, a));
+    double s, c;
+    sincos(r, &s, &c);
+    const int q = int((long long)k & 3);
+    const double x = q & 1 ? c : s, y = q & 1 ? s : c;
+    *sn = q & 2 ? -x : x;
+    *cs = (q + 1) & 2 ? -y : y;
 }
 
 // ------------------------------------------------------------------ append
@@ -36,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
     constexpr int LPR = D / 8;              // lanes per row
     constexpr int RPP = kThreads / LPR;     // rows per pass
     constexpr int GL = LPR / 4;             // lanes per quantisation group
-    __shared__ float s_cos[kAppTok][64], s_sin[kAppTok][64];
+    __shared__ __align__(16) float s_cos[kAppTok][64], s_sin[kAppTok][64];
     __shared__ long long s_row[kAppTok];    // byte offset of the token's row of kv head 0, or -1
     __shared__ int s_pos[kAppTok];
     __shared__ __align__(16) uint8_t s_val[INT4 ? RPP : 1][INT4 ? D / 2 : 16];
@@ -44,6 +60,33 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
     const int tid = threadIdx.x;
     const int t0 = blockIdx.x * tok_per_cta;
     const int nt = min(tok_per_cta, p.T - t0);
+    const int Hkv = p.kv.Hkv, Hq = p.q ? p.Hq : 0;
+    const int rows = Hq + 2 * Hkv;          // rows of a token: queries, keys, values
+    const int c = tid % LPR;                // this lane's 8 channels: [8c, 8c + 8)
+    const int total = nt * rows;
+    const long long head_bytes = (long long)p.kv.row_bytes << p.kv.page_shift;
+    // row ri of the CTA: token, kind (query, key, value), head
+    struct Row { int t, kind, h; };
+    auto row_of = [&](int ri) -> Row {
+        Row o;
+        o.t = min(ri / rows, nt - 1);
+        const int r = ri - o.t * rows;
+        o.kind = r < Hq ? 0 : r < Hq + Hkv ? 1 : 2;
+        o.h = o.kind == 0 ? r : o.kind == 1 ? r - Hq : r - Hq - Hkv;
+        return o;
+    };
+    auto fetch = [&](int ri) -> uint4 {
+        if (ri >= total) return make_uint4(0, 0, 0, 0);
+        const Row o = row_of(ri);
+        const uint16_t* src = o.kind == 0   ? p.q + (t0 + o.t) * p.q_tok + o.h * p.q_head
+                              : o.kind == 1 ? p.k + (t0 + o.t) * p.k_tok + o.h * p.k_head
+                                            : p.v + (t0 + o.t) * p.v_tok + o.h * p.v_head;
+        return __ldg(reinterpret_cast<const uint4*>(src) + c);
+    };
+    // the rows of the next passes are always on their way, the first ones before the token is looked up
+    uint4 ahead[kAppAhead];
+#pragma unroll
+    for (int i = 0; i < kAppAhead; ++i) ahead[i] = fetch(i * RPP + tid / LPR);
     if (tid < nt) {
         const int t = t0 + tid;
         long long row = -1;
@@ -67,36 +110,30 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
         const int t = i / half, f = i - t * half;
         if (s_row[t] < 0) continue;
         double sn, cs;
-        sincos(double(s_pos[t]) * double(p.inv_freq[f]), &sn, &cs);
+        angle_sincos(double(s_pos[t]) * double(p.inv_freq[f]), &sn, &cs);
         s_cos[t][f] = float(cs);
         s_sin[t][f] = float(sn);
     }
     __syncthreads();
 
-    const int Hkv = p.kv.Hkv, Hq = p.q ? p.Hq : 0;
-    const int rows = Hq + 2 * Hkv;          // rows of a token: queries, keys, values
-    const int c = tid % LPR;                // this lane's 8 channels: [8c, 8c + 8)
-    const int total = nt * rows;
-    const long long head_bytes = (long long)p.kv.row_bytes << p.kv.page_shift;
-    for (int base = 0; base < total; base += RPP) {   // same trip count for every lane: shuffles below
+    for (int base0 = 0; base0 < total; base0 += kAppAhead * RPP) {   // same trip count for every lane: shuffles below
+#pragma unroll
+      for (int pass = 0; pass < kAppAhead; ++pass) {
+        const int base = base0 + pass * RPP;
+        if (base >= total) break;           // (uniform)
         const int ri = base + tid / LPR;
-        const int t = min(ri / rows, nt - 1), r = ri - t * rows;
+        const Row row = row_of(ri);
+        const int t = row.t, kind = row.kind, h = row.h;
         const bool live = ri < total && s_row[t] >= 0;
-        const int kind = r < Hq ? 0 : r < Hq + Hkv ? 1 : 2;   // query, key, value
-        const int h = kind == 0 ? r : kind == 1 ? r - Hq : r - Hq - Hkv;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (live) {
-            const uint16_t* src = kind == 0   ? p.q + (t0 + t) * p.q_tok + h * p.q_head
-                                  : kind == 1 ? p.k + (t0 + t) * p.k_tok + h * p.k_head
-                                              : p.v + (t0 + t) * p.v_tok + h * p.v_head;
-            w = __ldg(reinterpret_cast<const uint4*>(src) + c);
-        }
+        const uint4 w = ahead[pass];
+        ahead[pass] = fetch(ri + kAppAhead * RPP);
         float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y), bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
         if (p.interleaved) {
             if (kind < 2 && 8 * c < p.rot) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float cs = s_cos[t][4 * c + j], sn = s_sin[t][4 * c + j];
+                    const float cs = f4(*reinterpret_cast<const float4*>(&s_cos[t][4 * c]), j);
+                    const float sn = f4(*reinterpret_cast<const float4*>(&s_sin[t][4 * c]), j);
                     const float a = x[2 * j], b = x[2 * j + 1];
                     x[2 * j] = __fsub_rn(__fmul_rn(a, cs), __fmul_rn(b, sn));
                     x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs), __fmul_rn(a, sn));
@@ -118,7 +155,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
                 const int f0 = (c < hc ? c : c - hc) * 8;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float cs = s_cos[t][f0 + j], sn = s_sin[t][f0 + j];
+                    const float cs = f4(*reinterpret_cast<const float4*>(&s_cos[t][f0 + (j & 4)]), j & 3);
+                    const float sn = f4(*reinterpret_cast<const float4*>(&s_sin[t][f0 + (j & 4)]), j & 3);
                     x[j] = c < hc ? __fsub_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn))
                                   : __fadd_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn));
                 }
@@ -133,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
                 reinterpret_cast<uint4*>(dst)[c] = o;
             }
         }
-        if constexpr (INT4) {
+        if (INT4 && __any_sync(0xffffffffu, kind > 0)) {
             // group maximum; an element that is not finite poisons the group
             float top = 0.f;
             bool bad = false;
@@ -149,11 +187,17 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
             const bool fin = top <= 3.402823466e38f;
             const uint32_t sb = fin ? (__float_as_uint(__fdiv_rn(top, 7.f)) + 0xffffu) & 0xffff0000u : 0x7fc00000u;
             const float s = __uint_as_float(sb);
+            // rint(x / s) + 8 in the low bits of y + (1.5 * 2^23 + 8), y = x * (1 / s): y is off by less than 2^-20,
+            // so only where it is that near to a border is the quotient itself needed
+            const float rs = __frcp_rn(s);
             uint32_t nib = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const int code = fin && s > 0.f ? __float2int_rn(__fdiv_rn(x[j], s)) : 0;
-                nib |= uint32_t(code + 8) << (4 * j);
+                const float y = x[j] * rs;
+                float z = __fadd_rn(y, 12582920.f);
+                if (!(fabsf(__fsub_rn(y, __fsub_rn(z, 12582920.f))) < 0.49999f))
+                    z = __fadd_rn(fin && s > 0.f ? __fdiv_rn(x[j], s) : 0.f, 12582920.f);
+                nib |= (__float_as_uint(z) & 15u) << (4 * j);
             }
             uint8_t* dst = p.kv.data + (live ? s_row[t] + h * head_bytes : 0);
             const int g = c / GL;
@@ -181,76 +225,133 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
             if (kind == 2 && live && c < D / 32)
                 *reinterpret_cast<uint4*>(dst + D / 2 + 16 * c) = *reinterpret_cast<const uint4*>(sv + 16 * c);
         }
+      }
     }
 }
 
 // ------------------------------------------------------------------ gather
-// One CTA per 64 tokens of one (sequence, kv head): the rows' bytes are staged in shared memory with
-// 16-byte loads and written as 16-byte pieces of the dense rows.
-constexpr int kGatTok = 64;
+// One warp per 16 tokens of one (sequence, kv head), without block barriers: the lanes look up the rows,
+// keep 5 (d = 128) 16-byte loads each in flight into the warp's shared memory, and write dense rows.
+constexpr int kGatTok = 16, kGatWarps = 4;
 
 template <int D, bool INT4>
-__global__ void __launch_bounds__(kThreads) paged_gather_kernel(PagedGatherParams p) {
+__global__ void __launch_bounds__(kGatWarps * 32) paged_gather_kernel(PagedGatherParams p) {
     constexpr int ROWB = INT4 ? D + 16 : 4 * D;
     constexpr int LPR = D / 8;
-    __shared__ long long s_row[kGatTok];
-    __shared__ __align__(16) uint8_t s_in[INT4 ? kGatTok * ROWB : 16];
+    // the unpacked rows go out by way of shared memory too, so that a warp's stores are whole rows
+    constexpr int OROW = 2 * D + 16;
+    __shared__ __align__(16) uint8_t s_in[INT4 ? kGatWarps : 1][INT4 ? kGatTok * ROWB : 16];
+    __shared__ __align__(16) uint8_t s_out[INT4 ? kGatWarps : 1][INT4 ? kGatTok * OROW : 16];
     pdl_enter();
-    const int tid = threadIdx.x;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = blockIdx.y, b = blockIdx.z;
-    const long long i0 = (long long)blockIdx.x * kGatTok;
+    const long long i0 = ((long long)blockIdx.x * kGatWarps + warp) * kGatTok;
+    if (i0 >= p.N) return;
     bool bad = false;
     const int len = paged_len(p.kv, p.kv.kv_len[b], &bad);
     const long long first = p.start ? p.start[b] : 0;
-    if (tid < kGatTok) {
-        long long row = -1;
-        const long long i = i0 + tid, n = first + i;
-        if (i < p.N && n >= 0 && n < len) {
+    long long row = -1;                     // of token i0 + lane (lanes 0-15)
+    {
+        const long long i = i0 + lane, n = first + i;
+        if (lane < kGatTok && i < p.N && n >= 0 && n < len) {
             row = paged_row(p.kv, p.kv.page_table[paged_slot(p.kv, b, n)], g, n);
             bad |= row < 0;
         }
-        s_row[tid] = row;
         if (bad || first < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
     }
-    __syncthreads();
     uint16_t* const outs[2] = {p.K, p.V};
+    const size_t out0 = (size_t(b) * p.kv.Hkv + g) * p.N + i0;
     if constexpr (INT4) {
-        constexpr int CH = ROWB / 16;
-        for (int i = tid; i < kGatTok * CH; i += kThreads) {
-            const int t = i / CH, ch = i - t * CH;
-            if (s_row[t] >= 0)
-                reinterpret_cast<uint4*>(s_in)[i] = __ldg(reinterpret_cast<const uint4*>(p.kv.data + s_row[t]) + ch);
-        }
-        __syncthreads();
-    }
-    for (int i = tid; i < kGatTok * 2 * LPR; i += kThreads) {
-        const int t = i / (2 * LPR), r = i - t * 2 * LPR, isv = r / LPR, c = r - isv * LPR;
-        if (s_row[t] < 0) continue;
-        uint4 o;
-        if constexpr (INT4) {
-            const uint8_t* row = s_in + t * ROWB;
-            const int gr = c / (LPR / 4);
-            const float s = bf_lo(reinterpret_cast<const uint16_t*>(row + D)[isv * 4 + gr]);
-            uint32_t nib;
-            if (!isv) {
-                if constexpr (D == 128) nib = *reinterpret_cast<const uint32_t*>(row + (c % 4) * 16 + gr * 4);
-                else
-                    nib = *reinterpret_cast<const uint16_t*>(row + (c % 2) * 16 + gr * 2) |
-                          uint32_t(*reinterpret_cast<const uint16_t*>(row + (c % 2) * 16 + 8 + gr * 2)) << 16;
-            } else {
-                nib = 0;
+        constexpr int CH = ROWB / 16, NL = (kGatTok * CH + 31) / 32;
+        uint4 w[NL];
 #pragma unroll
-                for (int r8 = 0; r8 < 8; ++r8)
-                    nib |= ((uint32_t(row[D / 2 + r8 * (D / 16) + c / 2]) >> (4 * (c & 1))) & 15u) << (4 * r8);
+        for (int j = 0; j < NL; ++j) {
+            const int i = lane + 32 * j, t = min(i / CH, kGatTok - 1), ch = i - t * CH;
+            const long long r = __shfl_sync(0xffffffffu, row, t);
+            w[j] = make_uint4(0, 0, 0, 0);
+            if (i < kGatTok * CH && r >= 0) w[j] = __ldg(reinterpret_cast<const uint4*>(p.kv.data + r) + ch);
+        }
+#pragma unroll
+        for (int j = 0; j < NL; ++j)
+            if (lane + 32 * j < kGatTok * CH) reinterpret_cast<uint4*>(s_in[warp])[lane + 32 * j] = w[j];
+        __syncwarp();
+        // A lane takes one group (d/4 channels) of a token's key and value.  A code u in the low bits of bf16 128 is
+        // 128 + u; minus 136 it is u - 8, both exact, and the product with the scale is rounded once.
+        auto value2 = [](uint32_t nib2, uint32_t s2) -> uint32_t {   // two codes in bits 0-3 and 16-19
+            uint32_t r;
+            asm("{\n .reg .b32 t;\n sub.rn.bf16x2 t, %1, %2;\n mul.rn.bf16x2 %0, t, %3;\n}\n"
+                : "=r"(r)
+                : "r"((nib2 & 0x000f000fu) | 0x43004300u), "r"(0x43084308u), "r"(s2));
+            return r;
+        };
+        const int gr = lane & 3;
+#pragma unroll
+        for (int isv = 0; isv < 2; ++isv) {
+#pragma unroll
+            for (int t0 = 0; t0 < kGatTok; t0 += 8) {
+                const int t = t0 + (lane >> 2);
+                const uint8_t* src = s_in[warp] + t * ROWB;
+                const uint32_t sc = reinterpret_cast<const uint16_t*>(src + D)[isv * 4 + gr], s2 = sc | sc << 16;
+                uint32_t o[D / 8];                     // the group's channel pairs
+                if (!isv) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) { // eight codes: channels 8 q .. 8 q + 7
+                        const uint32_t w =
+                            D == 128 ? *reinterpret_cast<const uint32_t*>(src + q * 16 + gr * 4)
+                                     : *reinterpret_cast<const uint16_t*>(src + q * 16 + gr * 2) |
+                                           uint32_t(*reinterpret_cast<const uint16_t*>(src + q * 16 + 8 + gr * 2)) << 16;
+                        uint32_t v[4];                 // codes k and k + 4
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = value2(w >> (4 * k), s2);
+                        o[4 * q] = __byte_perm(v[0], v[1], 0x5410);
+                        o[4 * q + 1] = __byte_perm(v[2], v[3], 0x5410);
+                        o[4 * q + 2] = __byte_perm(v[0], v[1], 0x7632);
+                        o[4 * q + 3] = __byte_perm(v[2], v[3], 0x7632);
+                    }
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {      // channels 2 r, 2 r + 1 of every eight
+                        const uint8_t* b0 = src + D / 2 + 2 * r * (D / 16) + gr * (D / 64);
+                        const uint32_t x = D == 128 ? *reinterpret_cast<const uint16_t*>(b0) : *b0;
+                        const uint32_t y = D == 128 ? *reinterpret_cast<const uint16_t*>(b0 + D / 16) : *(b0 + D / 16);
+                        const uint32_t w = x | y << 16;
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) o[4 * k + r] = value2(w >> (4 * k), s2);
+                    }
+                }
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+                    *reinterpret_cast<uint4*>(s_out[warp] + t * OROW + gr * (D / 2) + 16 * q) =
+                        make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
             }
-            float x[8];
+            __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] = float(int((nib >> (4 * j)) & 15u) - 8) * s;
-            o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-        } else {
-            o = __ldg(reinterpret_cast<const uint4*>(p.kv.data + s_row[t] + isv * 2 * D) + c);
+            for (int j = 0; j < kGatTok * LPR / 32; ++j) {
+                const int i = lane + 32 * j, t = i / LPR, c = i - t * LPR;
+                const bool live = __shfl_sync(0xffffffffu, int(row >= 0), t);
+                const uint4 v = *reinterpret_cast<const uint4*>(s_out[warp] + t * OROW + 16 * c);
+                if (live) reinterpret_cast<uint4*>(outs[isv] + (out0 + t) * D)[c] = v;
+            }
+            __syncwarp();
         }
-        reinterpret_cast<uint4*>(outs[isv] + ((size_t(b) * p.kv.Hkv + g) * p.N + i0 + t) * D)[c] = o;
+    } else {
+        constexpr int CH = 2 * LPR, NL = kGatTok * CH / 32;    // pieces of a row, loads per lane
+#pragma unroll
+        for (int j0 = 0; j0 < NL; j0 += 4) {
+            uint4 w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = lane + 32 * (j0 + j), t = i / CH, r = i - t * CH;
+                const long long at = __shfl_sync(0xffffffffu, row, t);
+                if (at >= 0) w[j] = __ldg(reinterpret_cast<const uint4*>(p.kv.data + at) + r);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int i = lane + 32 * (j0 + j), t = i / CH, r = i - t * CH, isv = r / LPR;
+                const long long at = __shfl_sync(0xffffffffu, row, t);
+                if (at >= 0) reinterpret_cast<uint4*>(outs[isv] + (out0 + t) * D)[r - isv * LPR] = w[j];
+            }
+        }
     }
 }
 
@@ -270,10 +371,11 @@ spa_status launch_paged_append(const PagedAppendParams& p, cudaStream_t st) {
 }
 
 spa_status launch_paged_gather(const PagedGatherParams& p, cudaStream_t st) {
-    const dim3 grid((p.N + kGatTok - 1) / kGatTok, p.kv.Hkv, p.kv.B);
+    constexpr int kPer = kGatTok * kGatWarps;
+    const dim3 grid((p.N + kPer - 1) / kPer, p.kv.Hkv, p.kv.B);
 #define SPA_GAT(DD, I4)                                                                       \
     if (p.kv.d == DD && (p.kv.int4 != 0) == I4)                                               \
-        SPA_CUDA_TRY(launch_pdl(paged_gather_kernel<DD, I4>, grid, dim3(kThreads), 0, st, p));
+        SPA_CUDA_TRY(launch_pdl(paged_gather_kernel<DD, I4>, grid, dim3(kGatWarps * 32), 0, st, p));
     SPA_GAT(64, false) SPA_GAT(64, true) SPA_GAT(128, false) SPA_GAT(128, true)
 #undef SPA_GAT
     return SPA_OK;
