@@ -48,7 +48,7 @@ __device__ __forceinline__ void angle_sincos(double a, double* sn, double* cs) {
 
 // ------------------------------------------------------------------ append
 template <int D, bool INT4>
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParams p, int tok_per_cta) {
+__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(PagedAppendParams p, int tok_per_cta) {
     constexpr int LPR = D / 8;              // lanes per row
     constexpr int RPP = kThreads / LPR;     // rows per pass
     constexpr int GL = LPR / 4;             // lanes per quantisation group
@@ -65,28 +65,30 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
     const int c = tid % LPR;                // this lane's 8 channels: [8c, 8c + 8)
     const int total = nt * rows;
     const long long head_bytes = (long long)p.kv.row_bytes << p.kv.page_shift;
-    // row ri of the CTA: token, kind (query, key, value), head
-    struct Row { int t, kind, h; };
-    auto row_of = [&](int ri) -> Row {
-        Row o;
-        o.t = min(ri / rows, nt - 1);
-        const int r = ri - o.t * rows;
-        o.kind = r < Hq ? 0 : r < Hq + Hkv ? 1 : 2;
-        o.h = o.kind == 0 ? r : o.kind == 1 ? r - Hq : r - Hq - Hkv;
-        return o;
+    // A cursor over the CTA's rows, RPP at a time: token t, row r of the token.
+    struct Cursor { int t, r; };
+    auto step = [&](Cursor& u) {
+        u.r += RPP;
+        while (u.r >= rows) { u.r -= rows; ++u.t; }
     };
-    auto fetch = [&](int ri) -> uint4 {
-        if (ri >= total) return make_uint4(0, 0, 0, 0);
-        const Row o = row_of(ri);
-        const uint16_t* src = o.kind == 0   ? p.q + (t0 + o.t) * p.q_tok + o.h * p.q_head
-                              : o.kind == 1 ? p.k + (t0 + o.t) * p.k_tok + o.h * p.k_head
-                                            : p.v + (t0 + o.t) * p.v_tok + o.h * p.v_head;
+    auto fetch = [&](const Cursor& u) -> uint4 {
+        if (u.t >= nt) return make_uint4(0, 0, 0, 0);
+        const int kv = u.r - Hq;
+        const uint16_t* src = kv < 0     ? p.q + (t0 + u.t) * p.q_tok + u.r * p.q_head
+                              : kv < Hkv ? p.k + (t0 + u.t) * p.k_tok + kv * p.k_head
+                                         : p.v + (t0 + u.t) * p.v_tok + (kv - Hkv) * p.v_head;
         return __ldg(reinterpret_cast<const uint4*>(src) + c);
     };
+    Cursor now{0, tid / LPR}, next;
+    while (now.r >= rows) { now.r -= rows; ++now.t; }
+    next = now;
     // the rows of the next passes are always on their way, the first ones before the token is looked up
     uint4 ahead[kAppAhead];
 #pragma unroll
-    for (int i = 0; i < kAppAhead; ++i) ahead[i] = fetch(i * RPP + tid / LPR);
+    for (int i = 0; i < kAppAhead; ++i) {
+        ahead[i] = fetch(next);
+        step(next);
+    }
     if (tid < nt) {
         const int t = t0 + tid;
         long long row = -1;
@@ -116,116 +118,120 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(PagedAppendParam
     }
     __syncthreads();
 
-    for (int base0 = 0; base0 < total; base0 += kAppAhead * RPP) {   // same trip count for every lane: shuffles below
+    const int hc = p.rot / 16;              // lanes per half of the rotated channels
+    const bool turn = p.interleaved ? 8 * c < p.rot : c < 2 * hc;
+    const int mate = !turn ? c : c < hc ? c + hc : c - hc;        // the lane with the pair partners
+    const int f0 = p.interleaved ? 4 * c : (c < hc ? c : c - hc) * 8;
+    for (int base = 0; base < total; base += kAppAhead * RPP) {   // same trip count for every lane: shuffles below
 #pragma unroll
-      for (int pass = 0; pass < kAppAhead; ++pass) {
-        const int base = base0 + pass * RPP;
-        if (base >= total) break;           // (uniform)
-        const int ri = base + tid / LPR;
-        const Row row = row_of(ri);
-        const int t = row.t, kind = row.kind, h = row.h;
-        const bool live = ri < total && s_row[t] >= 0;
-        const uint4 w = ahead[pass];
-        ahead[pass] = fetch(ri + kAppAhead * RPP);
-        float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y), bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
-        if (p.interleaved) {
-            if (kind < 2 && 8 * c < p.rot) {
+        for (int pass = 0; pass < kAppAhead; ++pass) {
+            if (base + pass * RPP >= total) break;                // (uniform)
+            const uint4 w = ahead[pass];
+            ahead[pass] = fetch(next);
+            step(next);
+            const int t = min(now.t, nt - 1), kv = now.r - Hq;
+            const int kind = kv < 0 ? 0 : kv < Hkv ? 1 : 2, h = kv < 0 ? now.r : kv < Hkv ? kv : kv - Hkv;
+            const bool live = now.t < nt && s_row[t] >= 0;
+            step(now);
+            float x[8] = {bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y), bf_lo(w.z), bf_hi(w.z), bf_lo(w.w), bf_hi(w.w)};
+            if (p.rot > 0 && __any_sync(0xffffffffu, kind < 2)) {
+                if (p.interleaved) {
+                    if (kind < 2 && turn) {
+                        const float4 cs = *reinterpret_cast<const float4*>(&s_cos[t][f0]);
+                        const float4 sn = *reinterpret_cast<const float4*>(&s_sin[t][f0]);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float cs = f4(*reinterpret_cast<const float4*>(&s_cos[t][4 * c]), j);
-                    const float sn = f4(*reinterpret_cast<const float4*>(&s_sin[t][4 * c]), j);
-                    const float a = x[2 * j], b = x[2 * j + 1];
-                    x[2 * j] = __fsub_rn(__fmul_rn(a, cs), __fmul_rn(b, sn));
-                    x[2 * j + 1] = __fadd_rn(__fmul_rn(b, cs), __fmul_rn(a, sn));
+                        for (int j = 0; j < 4; ++j) {
+                            const float a = x[2 * j], b = x[2 * j + 1];
+                            x[2 * j] = __fsub_rn(__fmul_rn(a, f4(cs, j)), __fmul_rn(b, f4(sn, j)));
+                            x[2 * j + 1] = __fadd_rn(__fmul_rn(b, f4(cs, j)), __fmul_rn(a, f4(sn, j)));
+                        }
+                    }
+                } else {
+                    const int src = (tid & 31) - c + mate;
+                    const uint32_t flip = c < hc ? 0x80008000u : 0u;   // x cos - y sin, or x cos + y sin
+                    uint4 o;
+                    o.x = __shfl_sync(0xffffffffu, w.x, src) ^ flip;
+                    o.y = __shfl_sync(0xffffffffu, w.y, src) ^ flip;
+                    o.z = __shfl_sync(0xffffffffu, w.z, src) ^ flip;
+                    o.w = __shfl_sync(0xffffffffu, w.w, src) ^ flip;
+                    if (kind < 2 && turn) {
+                        const float y[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
+                                            bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
+#pragma unroll
+                        for (int j4 = 0; j4 < 8; j4 += 4) {
+                            const float4 cs = *reinterpret_cast<const float4*>(&s_cos[t][f0 + j4]);
+                            const float4 sn = *reinterpret_cast<const float4*>(&s_sin[t][f0 + j4]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                x[j4 + j] = __fadd_rn(__fmul_rn(x[j4 + j], f4(cs, j)), __fmul_rn(y[j4 + j], f4(sn, j)));
+                        }
+                    }
                 }
             }
-        } else if (p.rot > 0) {
-            const int hc = p.rot / 16;      // lanes per half of the rotated channels
-            const bool turn = c < 2 * hc;
-            const int mate = !turn ? c : c < hc ? c + hc : c - hc;
-            const int src = (threadIdx.x & 31) - c % 32 + mate;   // the partner lane of the same row
-            uint4 o;
-            o.x = __shfl_sync(0xffffffffu, w.x, src);
-            o.y = __shfl_sync(0xffffffffu, w.y, src);
-            o.z = __shfl_sync(0xffffffffu, w.z, src);
-            o.w = __shfl_sync(0xffffffffu, w.w, src);
-            if (kind < 2 && turn) {
-                const float y[8] = {bf_lo(o.x), bf_hi(o.x), bf_lo(o.y), bf_hi(o.y),
-                                    bf_lo(o.z), bf_hi(o.z), bf_lo(o.w), bf_hi(o.w)};
-                const int f0 = (c < hc ? c : c - hc) * 8;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float cs = f4(*reinterpret_cast<const float4*>(&s_cos[t][f0 + (j & 4)]), j & 3);
-                    const float sn = f4(*reinterpret_cast<const float4*>(&s_sin[t][f0 + (j & 4)]), j & 3);
-                    x[j] = c < hc ? __fsub_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn))
-                                  : __fadd_rn(__fmul_rn(x[j], cs), __fmul_rn(y[j], sn));
-                }
-            }
-        }
-        if (kind == 0 || !INT4) {
-            if (live) {
+            if ((kind == 0 || !INT4) && live) {
                 const uint4 o = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
                                            pack_bf16(x[6], x[7]));
                 uint8_t* dst = kind == 0 ? reinterpret_cast<uint8_t*>(p.q_out + (size_t(t0 + t) * p.Hq + h) * D)
                                          : p.kv.data + s_row[t] + h * head_bytes + (kind == 2 ? 2 * D : 0);
                 reinterpret_cast<uint4*>(dst)[c] = o;
             }
-        }
-        if (INT4 && __any_sync(0xffffffffu, kind > 0)) {
-            // group maximum; an element that is not finite poisons the group
-            float top = 0.f;
-            bool bad = false;
+            if (INT4 && __any_sync(0xffffffffu, kind > 0)) {
+                // group maximum; an element that is not finite (its magnitude's bits are the largest) poisons the group
+                uint32_t top = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                bad |= !(fabsf(x[j]) <= 3.402823466e38f);
-                top = fmaxf(top, fabsf(x[j]));
-            }
-            if (bad) top = __uint_as_float(0x7f800000u);
+                for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[j]) & 0x7fffffffu);
 #pragma unroll
-            for (int off = 1; off < GL; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            // up to bf16: the scale must not be below amax / 7, so that no code clamps
-            const bool fin = top <= 3.402823466e38f;
-            const uint32_t sb = fin ? (__float_as_uint(__fdiv_rn(top, 7.f)) + 0xffffu) & 0xffff0000u : 0x7fc00000u;
-            const float s = __uint_as_float(sb);
-            // rint(x / s) + 8 in the low bits of y + (1.5 * 2^23 + 8), y = x * (1 / s): y is off by less than 2^-20,
-            // so only where it is that near to a border is the quotient itself needed
-            const float rs = __frcp_rn(s);
-            uint32_t nib = 0;
+                for (int off = 1; off < GL; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+                // up to bf16: the scale must not be below amax / 7, so that no code clamps
+                const bool fin = top < 0x7f800000u;
+                const uint32_t sb =
+                    fin ? (__float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) + 0xffffu) & 0xffff0000u : 0x7fc00000u;
+                const float s = __uint_as_float(sb);
+                // rint(x / s) + 8 in the low bits of y + (1.5 * 2^23 + 8), y = x * (1 / s): y is off by less than
+                // 2^-20, so only where it is that near to a border is the quotient itself needed
+                const float rs = __frcp_rn(s);
+                uint32_t nib = 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float y = x[j] * rs;
-                float z = __fadd_rn(y, 12582920.f);
-                if (!(fabsf(__fsub_rn(y, __fsub_rn(z, 12582920.f))) < 0.49999f))
-                    z = __fadd_rn(fin && s > 0.f ? __fdiv_rn(x[j], s) : 0.f, 12582920.f);
-                nib |= (__float_as_uint(z) & 15u) << (4 * j);
-            }
-            uint8_t* dst = p.kv.data + (live ? s_row[t] + h * head_bytes : 0);
-            const int g = c / GL;
-            if (live && kind > 0 && c % GL == 0)
-                reinterpret_cast<uint16_t*>(dst + D)[(kind == 2 ? 4 : 0) + g] = uint16_t(sb >> 16);
-            if (kind == 1 && live) {
-                if constexpr (D == 128) {   // a lane's 8 channels are one lane-of-a-quad's share of its group
-                    *reinterpret_cast<uint32_t*>(dst + (c % 4) * 16 + g * 4) = nib;
-                } else {
-                    *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + g * 2) = uint16_t(nib);
-                    *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + 8 + g * 2) = uint16_t(nib >> 16);
+                for (int j = 0; j < 8; ++j) {
+                    const float y = x[j] * rs;
+                    float z = __fadd_rn(y, 12582920.f);
+                    if (!(fabsf(__fsub_rn(y, __fsub_rn(z, 12582920.f))) < 0.49999f))
+                        z = __fadd_rn(fin && s > 0.f ? __fdiv_rn(x[j], s) : 0.f, 12582920.f);
+                    nib |= (__float_as_uint(z) & 15u) << (4 * j);
+                }
+                uint8_t* dst = p.kv.data + (live ? s_row[t] + h * head_bytes : 0);
+                const int g = c / GL;
+                if (live && kind > 0 && c % GL == 0)
+                    reinterpret_cast<uint16_t*>(dst + D)[(kind == 2 ? 4 : 0) + g] = uint16_t(sb >> 16);
+                if (kind == 1 && live) {
+                    if constexpr (D == 128) {   // a lane's 8 channels are one lane-of-a-quad's share of its group
+                        *reinterpret_cast<uint32_t*>(dst + (c % 4) * 16 + g * 4) = nib;
+                    } else {
+                        *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + g * 2) = uint16_t(nib);
+                        *reinterpret_cast<uint16_t*>(dst + (c % 2) * 16 + 8 + g * 2) = uint16_t(nib >> 16);
+                    }
+                }
+                if (__any_sync(0xffffffffu, kind == 2)) {
+                    // channels 16 i + r and 16 i + r + 8 share byte r * D/16 + (c / 2): an even lane joins its
+                    // neighbour's codes to its own; the bytes go through shared memory and out in 16-byte stores
+                    const uint32_t other = __shfl_xor_sync(0xffffffffu, nib, 1);
+                    const uint32_t even = (nib & 0x0f0f0f0fu) | (other & 0x0f0f0f0fu) << 4;      // r = 0, 2, 4, 6
+                    const uint32_t odd = ((nib >> 4) & 0x0f0f0f0fu) | (other & 0xf0f0f0f0u);     // r = 1, 3, 5, 7
+                    uint8_t* sv = s_val[tid / LPR];
+                    if (c % 2 == 0) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            sv[2 * r * (D / 16) + c / 2] = uint8_t(even >> (8 * r));
+                            sv[(2 * r + 1) * (D / 16) + c / 2] = uint8_t(odd >> (8 * r));
+                        }
+                    }
+                    __syncwarp();
+                    if (kind == 2 && live && c < D / 32)
+                        *reinterpret_cast<uint4*>(dst + D / 2 + 16 * c) = *reinterpret_cast<const uint4*>(sv + 16 * c);
+                    __syncwarp();
                 }
             }
-            // values: channels 16 i + r and 16 i + r + 8 share byte r * D/16 + (c / 2), so an even lane joins its
-            // neighbour's codes to its own; the row's bytes go through shared memory and out in 16-byte stores
-            const uint32_t other = __shfl_xor_sync(0xffffffffu, nib, 1);
-            uint8_t* sv = s_val[tid / LPR];
-            __syncwarp();
-            if (c % 2 == 0) {
-#pragma unroll
-                for (int r8 = 0; r8 < 8; ++r8)
-                    sv[r8 * (D / 16) + c / 2] = uint8_t(((nib >> (4 * r8)) & 15u) | (((other >> (4 * r8)) & 15u) << 4));
-            }
-            __syncwarp();
-            if (kind == 2 && live && c < D / 32)
-                *reinterpret_cast<uint4*>(dst + D / 2 + 16 * c) = *reinterpret_cast<const uint4*>(sv + 16 * c);
         }
-      }
     }
 }
 
