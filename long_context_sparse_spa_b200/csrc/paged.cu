@@ -21,8 +21,12 @@ namespace spa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAppTok = 4;   // tokens per CTA: 4 x 64 angles are one per thread at d = 128
-constexpr int kAppAhead = 3; // passes whose loads are in flight
+constexpr int kAppTok = 8;   // most tokens per CTA
+constexpr int kAppCtas = 6;  // CTAs per SM
+// Passes whose loads are in flight besides the current one.  More of them cost registers, and so resident CTAs:
+// 1 with 6 CTAs per SM, 2 with 4 and 3 with 4 took 39.7, 39.2 and 41.4 us for 4096 tokens in 4 bits (with the
+// read-back) and 11.5, 12.5 and 12.4 us for seven bf16 prompts.
+constexpr int kAppAhead = 1;
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
@@ -48,7 +52,7 @@ __device__ __forceinline__ void angle_sincos(double a, double* sn, double* cs) {
 
 // ------------------------------------------------------------------ append
 template <int D, bool INT4>
-__global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(PagedAppendParams p, int tok_per_cta) {
+__global__ void __launch_bounds__(kThreads, kAppCtas) paged_append_kernel(PagedAppendParams p, int tok_per_cta) {
     constexpr int LPR = D / 8;              // lanes per row
     constexpr int RPP = kThreads / LPR;     // rows per pass
     constexpr int GL = LPR / 4;             // lanes per quantisation group
@@ -89,22 +93,33 @@ __global__ void __launch_bounds__(kThreads, 4) paged_append_kernel(PagedAppendPa
         ahead[i] = fetch(next);
         step(next);
     }
-    if (tid < nt) {
-        const int t = t0 + tid;
-        long long row = -1;
-        int rope = 0;
-        const int b = paged_seq_of(p.seq_start, p.kv.B, t);
-        if (b >= 0) {
-            // slot of the token: the last of the sequence's new tokens is token kv_len[b] - 1
-            const long long left = p.seq_start ? (long long)p.seq_start[b + 1] - t : 1;
-            const long long n = (long long)p.kv.kv_len[b] - left;
-            const long long slot = paged_slot(p.kv, b, n);
-            if (slot >= 0) row = paged_row(p.kv, p.kv.page_table[slot], 0, n);
-            if (row < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
-            rope = p.positions ? p.positions[t] : int(n);
+    if (tid < 32 * nt) {                    // a warp per token
+        const int lane = tid & 31, i = tid >> 5, t = t0 + i;
+        int b;
+        if (p.seq_start && p.kv.B <= 1024) {
+            // the sequence by counting the starts at or before t: the loads do not wait for one another
+            int n = 0;
+            for (int k = lane; k <= p.kv.B; k += 32) n += p.seq_start[k] <= t ? 1 : 0;
+            b = __reduce_add_sync(0xffffffffu, n) - 1;
+            if (b >= p.kv.B || b < 0 || p.seq_start[b] > t || t >= p.seq_start[b + 1]) b = -1;
+        } else {
+            b = paged_seq_of(p.seq_start, p.kv.B, t);
         }
-        s_row[tid] = row;
-        s_pos[tid] = rope;
+        if (lane == 0) {
+            long long row = -1;
+            int rope = 0;
+            if (b >= 0) {
+                // slot of the token: the last of the sequence's new tokens is token kv_len[b] - 1
+                const long long left = p.seq_start ? (long long)p.seq_start[b + 1] - t : 1;
+                const long long n = (long long)p.kv.kv_len[b] - left;
+                const long long slot = paged_slot(p.kv, b, n);
+                if (slot >= 0) row = paged_row(p.kv, p.kv.page_table[slot], 0, n);
+                if (row < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+                rope = p.positions ? p.positions[t] : int(n);
+            }
+            s_row[i] = row;
+            s_pos[i] = rope;
+        }
     }
     __syncthreads();
     const int half = p.rot / 2;
@@ -364,9 +379,9 @@ __global__ void __launch_bounds__(kGatWarps * 32) paged_gather_kernel(PagedGathe
 }  // namespace
 
 spa_status launch_paged_append(const PagedAppendParams& p, cudaStream_t st) {
-    // tokens per CTA: as few as fill the SMs (a decode step has one token per sequence), at most kAppTok
-    const int sms = device_info().num_sms;
-    const int tok = p.T >= 4 * sms ? kAppTok : p.T >= 2 * sms ? 2 : 1;
+    // tokens per CTA: as few as give one wave of resident CTAs (a decode step has one token per sequence)
+    const int wave = device_info().num_sms * kAppCtas, want = (p.T + wave - 1) / wave;
+    const int tok = want < 1 ? 1 : want > kAppTok ? kAppTok : want;
     const dim3 grid((p.T + tok - 1) / tok);
 #define SPA_APP(DD, I4)                                                                                   \
     if (p.kv.d == DD && (p.kv.int4 != 0) == I4)                                                           \
