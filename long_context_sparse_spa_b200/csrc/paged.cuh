@@ -42,16 +42,16 @@ struct PagedAttendParams {
     float* out_f32;
     float* lse;                 // [T, Hq]
     int* arrived;               // [CTAs]: finished shares of the split unit that starts in a CTA; 0 between calls
-    float* partials;            // [2 * CTAs][16][d + 2]
+    float* partials;            // [2 * CTAs] shares of split units
     uint32_t* status;
 };
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
-size_t paged_attend_scratch_bytes(int d);
+size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse);
 void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch);   // the workspace after its header
-// paged_chunk.cu: more than 16 rows per sequence on average, 4-bit rows
+// paged_chunk.cu: more than 32 rows per sequence on average, 4-bit rows
 inline bool paged_chunk_taken(int format, const void* seq_start, const void* idx, int T, int Hq, int Hkv, int B,
                               float sm_scale) {
-    return format == SPA_KV_INT4 && seq_start && !idx && sm_scale > 0.f && (long long)T * (Hq / Hkv) > 16ll * B;
+    return format == SPA_KV_INT4 && seq_start && !idx && sm_scale > 0.f && (long long)T * (Hq / Hkv) > 32ll * B;
 }
 spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_chunk_scratch_bytes(int d);

@@ -1,7 +1,7 @@
 // Exact softmax attention over a paged KV cache, bf16 or 4-bit: decode (one query per sequence), a few
 // drafted or chunked queries per sequence (causal among themselves), or decode restricted to supports.
 //
-// Work split: a unit is one tile of up to 16 (query, head) rows that share the keys of one (sequence,
+// Work split: a unit is one tile of up to 32 (query, head) rows that share the keys of one (sequence,
 // kv head), or one support.  Its keys are cut into tiles of TILE tokens; the tiles of all units form one
 // list (each unit charged kSeg tiles for its start-up and merge), split evenly over the CTAs (one per
 // SM).  Inside a CTA the warps take a unit's tiles round-robin; each warp copies its tiles into its own
@@ -37,7 +37,7 @@
 namespace spa {
 namespace {
 
-constexpr int kRowsMax = 16;              // (query, head) rows of a unit
+constexpr int kRowsMax = 32;              // (query, head) rows of a unit
 constexpr int kSeg = 32;                  // tiles charged to a unit for its start-up and merge
 constexpr int kShare = 16;                // least weighted tiles of a CTA's share
 constexpr float kLog2e = 1.4426950408889634f;
@@ -48,7 +48,7 @@ constexpr float kSlack = 6.f;             // the reference moves only when it is
 constexpr uint32_t kWaitLimit = 1u << 22;
 
 // floats of one share of a split unit
-__host__ __device__ constexpr int paged_rec_floats(int d) { return kRowsMax * (d + 2); }
+__host__ __device__ constexpr int paged_rec_floats(int d, int rows) { return rows * (d + 2); }
 
 template <int D, bool INT4, int NT>
 struct Geo {
@@ -56,8 +56,11 @@ struct Geo {
     static constexpr int TILE = INT4 ? 32 : 16;           // tokens per warp step
     static constexpr int MT = TILE / 16;
     static constexpr int STAGES = 3;
-    static constexpr int WARPS = 8;
+    static constexpr int WARPS = INT4 && NT == 2 ? 12 : 8;
     static constexpr int CTAS = INT4 && NT == 1 ? 2 : 1;  // per SM
+    // more than one column tile: the queries' operand fragments lie in shared memory, not in registers
+    static constexpr bool QS = NT > 1;
+    static constexpr int QBYTES = QS ? NT * (D / 16 + 3) * 256 : 0;
     // shared-memory row stride: bf16 rows are copied one by one and padded (a multiple of 128 bytes would put
     // the eight rows of a fragment on the same banks)
     static constexpr int SROW = INT4 ? ROWB : ROWB + 16;
@@ -65,7 +68,7 @@ struct Geo {
     // the warps' parts, their factors and (M, L); the merge of shares puts a factor of each over the parts
     static constexpr int MERGE = WARPS * NT * 8 * (D + 2) * 4 + NT * 8 * (WARPS + 2) * 4;
     static constexpr int PREP = INT4 ? WARPS * TILE * 8 : 0;   // (log2, 1 / value) of each token's largest value scale
-    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + PREP;
+    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + PREP + QBYTES;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -198,7 +201,10 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t* const ring = smem;
     uint32_t* const s_prefix = reinterpret_cast<uint32_t*>(smem + G_::SMEM);   // [groups + 1]
-    const uint32_t prep = smem_u32(smem + G_::SMEM - G_::PREP + (INT4 ? (threadIdx.x >> 5) * TILE * 8 : 0));
+    const uint32_t prep = smem_u32(smem + G_::SMEM - G_::PREP - G_::QBYTES + (INT4 ? (threadIdx.x >> 5) * TILE * 8 : 0));
+    // per column tile: KS k-steps of (b0, b1) by lane, then (qz0, qz1), (hs0, hs1) and the two columns' limits
+    constexpr bool QS = G_::QS;
+    const uint32_t qs = smem_u32(smem + G_::SMEM - G_::QBYTES) + (threadIdx.x & 31) * 8;
     __shared__ uint64_t s_full[kWarps][STAGES];
     __shared__ uint32_t s_vmask[kWarps][STAGES];
     __shared__ long long s_wsum[kWarps];
@@ -465,12 +471,15 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
 #pragma unroll 1
         for (int j = 0; j < STAGES - 1; ++j) advance();
         // ---- queries as the B operand of S (column n = r8 of column tile nt), zero beyond nrow
-        uint32_t qb[KS][NT][2];
-        float hs[NT][2];                        // logit scale (log2 units) of this lane's two columns
-        uint32_t qz[NT][2];                     // 4-bit: -8 sum q of each group in three bf16 terms, as a B operand
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int row = nt * 8 + r8;
+        constexpr int NR = QS ? 1 : NT;         // column tiles held in registers
+        uint32_t qb[KS][NR][2];
+        float hs[NR][2];                        // logit scale (log2 units) of this lane's two columns
+        uint32_t qz[NR][2];                     // 4-bit: -8 sum q of each group in three bf16 terms, as a B operand
+        int lim[NR][2];                         // keys that this lane's columns may see
+        qz[0][0] = qz[0][1] = 0;
+        for (int tile = QS ? warp : 0; tile < NT; tile += QS ? kWarps : 1) {   // QS: a warp per column tile
+            constexpr int nt = 0;
+            const int row = tile * 8 + r8;
             const bool v = row < nrow;
             const uint16_t* src =
                 p.q + (v ? (un.row0 + row / un.heads) * p.q_tok + (un.h0 + row % un.heads) * p.q_head : 0);
@@ -550,15 +559,45 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                 }
                 hs[nt][0] = hs[nt][1] = sl2;
             }
-        }
-        int lim[NT][2];                         // keys that this lane's columns may see
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int row = nt * 8 + 2 * t4 + e;
-                lim[nt][e] = row < nrow ? un.lim0 + row / un.heads : un.ntok;
+                const int col = tile * 8 + 2 * t4 + e;
+                lim[nt][e] = col < nrow ? un.lim0 + col / un.heads : un.ntok;
             }
+            if constexpr (QS) {
+                const uint32_t at = qs + tile * (KS + 3) * 256;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) sts64(at + k * 256, qb[k][0][0], qb[k][0][1]);
+                sts64(at + KS * 256, qz[0][0], qz[0][1]);
+                sts64(at + KS * 256 + 256, __float_as_uint(hs[0][0]), __float_as_uint(hs[0][1]));
+                sts64(at + KS * 256 + 512, uint32_t(lim[0][0]), uint32_t(lim[0][1]));
+            }
+        }
+        if constexpr (QS) __syncthreads();
+        auto q_frag = [&](int k, int nt) -> uint2 {
+            if constexpr (QS) return lds64(qs + (nt * (KS + 3) + k) * 256);
+            else return make_uint2(qb[k][nt][0], qb[k][nt][1]);
+        };
+        auto q_zero = [&](int nt) -> uint2 {
+            if constexpr (QS) return lds64(qs + (nt * (KS + 3) + KS) * 256);
+            else return make_uint2(qz[nt][0], qz[nt][1]);
+        };
+        auto q_scale = [&](int nt) -> float2 {
+            if constexpr (QS) {
+                const uint2 v = lds64(qs + (nt * (KS + 3) + KS + 1) * 256);
+                return make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+            } else {
+                return make_float2(hs[nt][0], hs[nt][1]);
+            }
+        };
+        auto q_lim = [&](int nt) -> int2 {
+            if constexpr (QS) {
+                const uint2 v = lds64(qs + (nt * (KS + 3) + KS + 2) * 256);
+                return make_int2(int(v.x), int(v.y));
+            } else {
+                return make_int2(lim[nt][0], lim[nt][1]);
+            }
+        };
 
         // ---- state of this warp: per column the reference m (-inf: no key yet), the sum l, and O^T
         float top_r[NT][2], off_r[NT][2], l_r[NT][2], acc[DT][NT][4];   // m + kSlack and kBase - m
@@ -604,6 +643,21 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
             const bool edge = vmask != (TILE == 32 ? 0xffffffffu : (1u << TILE) - 1u) ||
                               (!sparse && n0 + TILE > un.lim0);
 
+            // Values that are not finite among tokens that only some queries see (else a zero weight is enough)
+            bool poison = false;
+            if (edge && un.nq > 1) {
+                auto inf2 = [](uint32_t w) { return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u; };
+                if constexpr (INT4) {
+                    const uint2 v = lds64(st + lane * SROW + D + 8);
+                    poison = inf2(v.x) || inf2(v.y);
+                } else {
+                    for (int i = lane; i < TILE * (D / 8); i += 32) {
+                        const uint4 v = lds128(st + (i / (D / 8)) * SROW + 2 * D + (i % (D / 8)) * 16);
+                        poison |= inf2(v.x) || inf2(v.y) || inf2(v.z) || inf2(v.w);
+                    }
+                }
+                poison = __any_sync(0xffffffffu, poison);
+            }
             if constexpr (INT4) {
                 // One token per lane: its largest value scale that is a number (its bits twice: at most 2^-7 more),
                 // log2 and 1 / of it, and the scales relative to it as fp16 * 2^15, stored by token pairs over the
@@ -640,7 +694,10 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                         const uint32_t z0 = t4 & 1 ? sa.y : sa.x, z1 = t4 & 1 ? sb.y : sb.x;
                         const uint32_t f[4] = {z0, z1, z0, z1};
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], f, qz[nt][0], qz[nt][1]);
+                        for (int nt = 0; nt < NT; ++nt) {
+                            const uint2 z = q_zero(nt);
+                            mma16816(s[nt], f, z.x, z.y);
+                        }
                     }
                     {
                         const uint2 wa = lds64(prep + tk * 8), wb = lds64(prep + tk * 8 + 64);
@@ -672,10 +729,12 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                         for (int nt = 0; nt < NT; ++nt) {
                             float d[4] = {0.f, 0.f, 0.f, 0.f};
                             if constexpr (D == 128) {
-                                mma_f16(d, f0, qb[2 * g][nt][0], qb[2 * g][nt][1]);
-                                mma_f16(d, f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1]);
+                                const uint2 qa = q_frag(2 * g, nt), qc = q_frag(2 * g + 1, nt);
+                                mma_f16(d, f0, qa.x, qa.y);
+                                mma_f16(d, f1, qc.x, qc.y);
                             } else {
-                                mma_f16(d, f0, qb[g][nt][0], qb[g][nt][1]);
+                                const uint2 qa = q_frag(g, nt);
+                                mma_f16(d, f0, qa.x, qa.y);
                             }
                             s[nt][0] = fmaf(fa[g], d[0], s[nt][0]);
                             s[nt][1] = fmaf(fa[g], d[1], s[nt][1]);
@@ -691,8 +750,9 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                         const uint32_t f0[4] = {wa.x, wb.x, wa.y, wb.y}, f1[4] = {wa.z, wb.z, wa.w, wb.w};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816(s[nt], f0, qb[2 * g][nt][0], qb[2 * g][nt][1]);
-                            mma16816(s[nt], f1, qb[2 * g + 1][nt][0], qb[2 * g + 1][nt][1]);
+                            const uint2 qa = q_frag(2 * g, nt), qc = q_frag(2 * g + 1, nt);
+                            mma16816(s[nt], f0, qa.x, qa.y);
+                            mma16816(s[nt], f1, qc.x, qc.y);
                         }
                     }
                 }
@@ -700,12 +760,14 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                 bool up = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
+                    const float2 h = q_scale(nt);
+                    [[maybe_unused]] const int2 li = q_lim(nt);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s[nt][e] = fmaf(s[nt][e], hs[nt][e & 1], lgv[e >> 1]);
+                        s[nt][e] = fmaf(s[nt][e], e & 1 ? h.y : h.x, lgv[e >> 1]);
                         if constexpr (EDGE) {
                             const int tok = tk + (e >> 1) * 8;
-                            const bool see = ((vmask >> tok) & 1u) && (sparse || n0 + tok < lim[nt][e & 1]);
+                            const bool see = ((vmask >> tok) & 1u) && (sparse || n0 + tok < (e & 1 ? li.y : li.x));
                             s[nt][e] = see ? s[nt][e] : -INFINITY;
                         }
                     }
@@ -732,8 +794,8 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                             }
                         }
                 }
-                // Tokens that some of the queries do not see: one product per query token, with the values it does
-                // not see taken as 0 (0 * NaN would reach its sum).
+                // With such values: one product per query token, with what it does not see taken as 0 (0 * NaN would
+                // reach its sum).
                 auto edge_product = [&](const uint32_t (&f)[4], int dt, auto product) {
                     const int ka = n0 + mt * 16 + tau<D, INT4>(2 * t4), kb = n0 + mt * 16 + tau<D, INT4>(2 * t4 + 1);
                     for (int i = 0; i < un.nq; ++i) {
@@ -813,7 +875,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                                                        fma_f16x2(hi & 0x00780078u, rg[1][i], nl[1][i]),
                                                        fma_f16x2(hi & 0x07800780u, rg[1][i], nh[1][i])};
                                 const int dt = (2 * qq + q) * 2 + e;
-                                if (!EDGE || un.nq == 1) {
+                                if (!EDGE || !poison) {
 #pragma unroll
                                     for (int nt = 0; nt < NT; ++nt) mma_f16(acc[dt][nt], f, b0[nt], b1[nt]);
                                 } else {
@@ -843,7 +905,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                     for (int dt = 0; dt < DT; ++dt) {
                         uint32_t f[4];
                         ldsm_x4_t(vb + dt * 32, f[0], f[1], f[2], f[3]);
-                        if (!EDGE || un.nq == 1) {
+                        if (!EDGE || !poison) {
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
                                 mma16816(acc[dt][nt], f, ph[nt][0], ph[nt][1]);
@@ -934,9 +996,9 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
             ml[2 * tid + 1] = L;
         }
         __syncthreads();
-        // A unit's first share goes to slot 2c + 1 of its CTA, later shares to slot 2c.  A slot holds O [16][D],
-        // then (M, L) [16].
-        constexpr int REC = paged_rec_floats(D);
+        // A unit's first share goes to slot 2c + 1 of its CTA, later shares to slot 2c.  A slot holds O [ROWS][D],
+        // then (M, L) [ROWS].
+        constexpr int REC = paged_rec_floats(D, ROWS);
         float* const part = p.partials + size_t(2 * cta + (a == 0 ? 1 : 0)) * REC;
         for (int i = tid; i < nrow * (D / 4); i += kThreads) {
             const int row = i / (D / 4), c = 4 * (i % (D / 4));
@@ -953,7 +1015,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
         }
         if (tid < nrow) {
             if (whole) store_lse(tid, ml[2 * tid], ml[2 * tid + 1]);
-            else *reinterpret_cast<float2*>(part + kRowsMax * D + 2 * tid) = make_float2(ml[2 * tid], ml[2 * tid + 1]);
+            else *reinterpret_cast<float2*>(part + ROWS * D + 2 * tid) = make_float2(ml[2 * tid], ml[2 * tid + 1]);
         }
         if (!whole) {
             // the last CTA of a split unit to get here merges its shares, in the order of the CTAs
@@ -978,7 +1040,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                     for (int k0 = 0; k0 < n; k0 += 32) {   // running (M, L) over 32 shares at a time
                         const int k = k0 + lane;
                         float2 v = make_float2(-INFINITY, 0.f);
-                        if (k < n) v = __ldcg(reinterpret_cast<const float2*>(slot(k) + kRowsMax * D + 2 * row));
+                        if (k < n) v = __ldcg(reinterpret_cast<const float2*>(slot(k) + ROWS * D + 2 * row));
                         float m = v.x;
 #pragma unroll
                         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1026,11 +1088,25 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
 
 }  // namespace
 
-// Workspace after the header: [2 * SMs] arrival counters, then two shares of 16 rows for each CTA.
+// Column tiles of 8 (query, head) rows of a unit, and query tokens of a unit: one query per unit where there
+// are no more tokens than sequences, else as many as a sequence has on average, up to 32 rows.
+static void paged_shape(int T, int B, int heads, bool sparse, int* nt, int* TQ) {
+    int rows = heads;
+    if (!sparse && T > B) {
+        const long long avg = ((long long)T * heads + B - 1) / B;
+        rows = avg > kRowsMax ? kRowsMax : avg > heads ? int(avg) : heads;
+    }
+    *nt = (rows + 7) / 8;
+    *TQ = sparse || T <= B ? 1 : paged_tokens_per_tile(*nt * 8, heads);
+}
 static size_t paged_attend_grid_max() { return size_t(device_info().num_sms) * 2; }
-size_t paged_attend_scratch_bytes(int d) {
+
+// Workspace after the header: [2 * SMs] arrival counters, then two shares for each CTA.
+size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse) {
     const size_t grid = paged_attend_grid_max();
-    return align_up(grid * 4, 256) + align_up(2 * grid * paged_rec_floats(d) * 4, 256);
+    int nt, TQ;
+    paged_shape(T, B, heads, sparse, &nt, &TQ);
+    return align_up(grid * 4, 256) + align_up(2 * grid * paged_rec_floats(d, nt * 8) * 4, 256);
 }
 void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch) {
     p.arrived = reinterpret_cast<int*>(scratch);
@@ -1042,11 +1118,9 @@ spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
     const int sms = device_info().num_sms;
     const bool sparse = p.idx != nullptr;
     const int heads = sparse && p.collapse == SPA_COLLAPSE_NONE ? 1 : G;
-    if (heads > kRowsMax) return SPA_ERR_UNSUPPORTED_SHAPE;
     const long long all = !sparse ? p.kv.B : (long long)p.T * (p.collapse == SPA_COLLAPSE_GROUP_MEAN ? p.kv.Hkv : p.Hq);
-    // one query tile per token when there are no more tokens than sequences, else as many as fill 16 rows
-    const int TQ = sparse || p.T <= p.kv.B ? 1 : paged_tokens_per_tile(kRowsMax, G);
-    const int nt = TQ * heads > 8 ? 2 : 1;
+    int nt, TQ;
+    paged_shape(p.T, p.kv.B, heads, sparse, &nt, &TQ);
     // the prefix of a launch's groups lies in shared memory, so a launch takes at most kPagedMaxUnits of them
     // (and the weighted tiles of a launch are counted in 32 bits: a sequence's queries times its length bound them)
     const long long tiles = (((long long)p.kv.max_pages << p.kv.page_shift) + 15) / 16 + kSeg;
@@ -1062,13 +1136,15 @@ spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
     if (p.kv.d == DD && (p.kv.int4 != 0) == I4 && nt == NTT) {                                                   \
         using G_ = Geo<DD, I4, NTT>;                                                                             \
         constexpr size_t kMost = G_::SMEM + size_t(kPagedMaxUnits + 1) * 4;                                      \
+        static_assert(kMost + 1024 <= 227 * 1024, "paged attention: shared memory over the per-CTA limit");       \
         SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_attend_kernel<DD, I4, NTT>),              \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)));                   \
         SPA_CUDA_TRY(launch_pdl(paged_attend_kernel<DD, I4, NTT>, dim3(sms * G_::CTAS), dim3(G_::WARPS * 32),    \
                                 G_::SMEM + size_t(groups + 1) * 4, st, p, int(g0), groups, TQ));                 \
     }
-        SPA_PA(64, false, 1) SPA_PA(64, false, 2) SPA_PA(64, true, 1) SPA_PA(64, true, 2)
-        SPA_PA(128, false, 1) SPA_PA(128, false, 2) SPA_PA(128, true, 1) SPA_PA(128, true, 2)
+#define SPA_PN(DD, I4) SPA_PA(DD, I4, 1) SPA_PA(DD, I4, 2) SPA_PA(DD, I4, 3) SPA_PA(DD, I4, 4)
+        SPA_PN(64, false) SPA_PN(64, true) SPA_PN(128, false) SPA_PN(128, true)
+#undef SPA_PN
 #undef SPA_PA
     }
     return SPA_OK;
