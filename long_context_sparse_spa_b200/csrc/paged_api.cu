@@ -21,6 +21,8 @@ spa_status check_kv(const spa_paged_kv& kv, bool* noop, PagedView* v) {
     if (kv.B > 65535 || kv.Hkv > 65535) return SPA_ERR_UNSUPPORTED_SHAPE;
     int shift = 0;
     while ((1 << shift) < kv.page) ++shift;
+    // rows of the pool are counted in 32 bits (more would not fit a GPU)
+    if ((long long)kv.num_pages * kv.Hkv > (0xfffffffell >> shift)) return SPA_ERR_UNSUPPORTED_SHAPE;
     // lengths are 32-bit: tokens that a page table can name must be too
     if (((long long)kv.max_pages << shift) > INT_MAX - 4096) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (!kv.kv_len || (kv.max_pages > 0 && !kv.page_table) || (kv.num_pages > 0 && !kv.data)) return SPA_ERR_INVALID_ARG;

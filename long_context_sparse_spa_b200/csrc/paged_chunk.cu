@@ -13,9 +13,10 @@
 // rescaled through TMEM, only when it is exceeded by 2^6.  l is summed in fp32.
 //
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row), 8-15 unpack the cache (8-11 keys,
-// 12-15 values; a thread has half of a token's codes), 16 issues the MMAs.  While one row tile is in its softmax the
-// tensor cores work for the other.  Raw rows come by cp.async two steps of 64 tokens ahead; the unpacked
-// K and V tiles are double-buffered.  Each row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
+// 12-15 values; a thread has half of a token's codes), 16 and 17 issue the MMAs of row tile 0 and 1, 18 copies
+// raw rows.  While one row tile is in its softmax the
+// tensor cores work for the other.  Raw rows come by bulk copies, up to three steps of 64 tokens
+// ahead, one copy per run of tokens that lie together on a page; the unpacked K and V tiles are double-buffered.  Each row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
 // order, so an observed S(t) also means that P(t-1) V is complete and O may be read and rescaled.
 //
 // Units are split evenly over the SMs by 128-token tiles as in paged_attend.cu; the last CTA of a split
@@ -33,8 +34,9 @@ using namespace tc;
 constexpr int kKeys = 128;                // tokens per tile
 constexpr int kHalf = 64;                 // tokens per unpacking step
 constexpr int kUnpack = 8;                // unpacking warps
-constexpr int kThreads = (8 + kUnpack + 1) * 32;
+constexpr int kThreads = (8 + kUnpack + 3) * 32;
 constexpr int kSegC = 6;                  // tiles charged to a unit
+constexpr int kChunkUnits = 256;          // sequences of a launch: 4 bytes of shared memory each
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kBase = 9.f, kSlack = 6.f;
@@ -44,13 +46,15 @@ template <int D>
 struct ChunkShared {
     static constexpr int kSlabs = D / 64;
     static constexpr int kTile = kSlabs * kSlab;       // 128 rows of D fp16
-    static constexpr int ROWB = D + 16;
     uint8_t q[2][kTile];
     uint8_t k[2][kTile];
     uint8_t v[2][kTile];
+    static constexpr int ROWB = D + 16;
     uint8_t raw[3][kHalf * ROWB];
-    long long rowoff[4][kHalf];                        // byte offset of a step's rows in the cache, -1: none
-    uint64_t s_full[2], p_full[2], k_full[2], v_full[2], k_empty[2], v_empty[2], o_done, q_full;
+    uint64_t raw_full[3], raw_empty[3];
+    uint32_t raw_valid[3][2];                          // tokens of the step that exist
+    uint64_t s_full[2], p_full[2][2], pv_half[2];      // by row tile (and half of the tokens)
+    uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], o_done, q_full;
     int ek[4][2], ev[4][2];                            // the powers of two of tile t (slot t % 4), by half
     alignas(16) int8_t ek1[4][kKeys];                  // ... of a tile that not all queries see whole: by token
     alignas(16) int8_t ev1[4][kKeys];
@@ -59,7 +63,7 @@ struct ChunkShared {
     int fail;                                          // a bounded wait gave up
     int last;
     alignas(16) uint32_t valid[4][4];                  // tile t: tokens that exist
-    long long wsum[16];
+    long long wsum[kThreads / 32];
 };
 
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -78,6 +82,11 @@ __device__ __forceinline__ uint32_t fma_f16x2(uint32_t a, uint32_t b, uint32_t c
     uint32_t r;
     asm("fma.rn.f16x2 %0, %1, %2, %3;\n" : "=r"(r) : "r"(a), "r"(b), "r"(c));
     return r;
+}
+__device__ __forceinline__ bool elect_one() {          // one lane of a converged warp
+    uint32_t r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+    return r != 0;
 }
 __device__ __forceinline__ void arrive(uint64_t* bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(bar)) : "memory");
@@ -101,6 +110,22 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// 16 columns of this thread's TMEM lane, not to be used before ld_wait
+__device__ __forceinline__ void ld16_begin(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15}, [%16];\n"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void ld_wait(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
+                 : "memory");
+}
 // Fp16 pairs of scales s, and -8 s in the units of the two kinds of codes below.
 struct Scale2 {
     uint32_t s, lo, hi;
@@ -120,6 +145,29 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, const Scale2& a, const Scal
     const uint32_t x = w << 3, y = w >> 5;
     return make_uint4(fma_f16x2(x & 0x00780078u, a.s, a.lo), fma_f16x2(x & 0x07800780u, a.s, a.hi),
                       fma_f16x2(y & 0x00780078u, b.s, b.lo), fma_f16x2(y & 0x07800780u, b.s, b.hi));
+}
+
+// paired fp32 arithmetic (one instruction for two lanes of a 64-bit register pair)
+__device__ __forceinline__ void ffma2(float& r0, float& r1, float b, float c) {   // r * b + c
+    asm("{\n .reg .b64 a, x, y;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%2, %2};\n mov.b64 y, {%3, %3};\n"
+        " fma.rn.f32x2 a, a, x, y;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(r0), "+f"(r1)
+        : "f"(b), "f"(c));
+}
+__device__ __forceinline__ void fadd2(float& r0, float& r1, float a0, float a1) {
+    asm("{\n .reg .b64 a, x;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%2, %3};\n add.f32x2 a, a, x;\n mov.b64 {%0, %1}, a;\n}\n"
+        : "+f"(r0), "+f"(r1)
+        : "f"(a0), "f"(a1));
+}
+__device__ __forceinline__ uint32_t max_f16x2(uint32_t a, uint32_t b) {   // of a number and a NaN the number
+    uint32_t r;
+    asm("max.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // floats of one share of a split unit: O [D / 4][256][4], then m, l and the poisoned groups of each row
@@ -147,12 +195,12 @@ __device__ __forceinline__ long long head_weight(const SeqG& s, int TQ) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
     using SH = ChunkShared<D>;
-    static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && offsetof(SH, rowoff) % 8 == 0 &&
+    static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && SH::ROWB % 16 == 0 && offsetof(SH, ek1) % 16 == 0 &&
                   sizeof(SH) % 8 == 0, "alignment of shared accesses");
-    constexpr int ROWB = SH::ROWB, WORDS = D / 8;      // 16-byte pieces of an operand row, code words of a row
+    constexpr int WORDS = D / 8;                       // 16-byte pieces of an operand row, code words of a row
     extern __shared__ __align__(1024) uint8_t dyn[];
     SH& sh = *reinterpret_cast<SH*>(dyn);
-    long long* const s_prefix = reinterpret_cast<long long*>(dyn + sizeof(SH));   // [groups + 1]
+    uint32_t* const s_prefix = reinterpret_cast<uint32_t*>(dyn + sizeof(SH));   // [groups + 1]
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.Hq / p.kv.Hkv;
 
@@ -160,13 +208,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.p_full[i], 128);
+            for (int h = 0; h < 2; ++h) mbar_init(&sh.p_full[i][h], 128);
+            mbar_init(&sh.pv_half[i], 1);
             mbar_init(&sh.k_full[i], kUnpack);         // 4 warps x 2 steps
             mbar_init(&sh.v_full[i], kUnpack);
-            mbar_init(&sh.k_empty[i], 1);
-            mbar_init(&sh.v_empty[i], 1);
+            mbar_init(&sh.k_empty[i], 2);              // both row tiles are through with it
+            mbar_init(&sh.v_empty[i], 2);
         }
-        mbar_init(&sh.o_done, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&sh.raw_full[i], 1);
+            mbar_init(&sh.raw_empty[i], kUnpack);
+        }
+        mbar_init(&sh.o_done, 2);
         mbar_init(&sh.q_full, 256);
         sh.fail = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
@@ -199,11 +252,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             if (w < warp) before += sh.wsum[w];
             tot += sh.wsum[w];
         }
-        if (u < groups) s_prefix[u] = before + incl - t;
+        if (u < groups) s_prefix[u] = uint32_t(before + incl - t);
         running += tot;
         __syncthreads();
     }
-    if (tid == 0) s_prefix[groups] = running;
+    if (tid == 0) s_prefix[groups] = uint32_t(running);
     tc_fence_before();
     empties = __syncthreads_or(empties);               // (also: barriers initialised, TMEM allocated)
     tc_fence_after();
@@ -252,6 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
     }
     const float sl2 = p.sm_scale * kLog2e;
     // uses of the barriers so far, by role: tiles filled / consumed over all segments, and segments
+    uint32_t raw_done = 0;                             // steps of 64 tokens
     uint32_t tiles_done = 0, tiles1_done = 0, segs = 0;   // (tiles1: those in which row tile 1 took part)
 
     long long x = x0;
@@ -287,94 +341,36 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         }
         const int nt = bnd - a;
         const uint32_t base = tiles_done;              // tile index of this segment's first tile, over the kernel
-        const uint32_t base1 = tiles1_done;
+        const uint32_t base1 = tiles1_done, base_raw = raw_done;
+        raw_done += uint32_t(2 * nt);
         tiles_done += uint32_t(nt);
         if (ntile == 2) tiles1_done += uint32_t(nt);
 
         if (warp >= 8 && warp < 8 + kUnpack) {
             // ================================================================ unpacking
-            const int ut = tid - 256, uw = ut >> 5;    // 0 .. 255
-            const bool isv = uw >= 4;
-            const int part = (uw >> 1) & 1, tok = (uw & 1) * 32 + lane;
-            // 16-byte pieces of a step's rows that this thread copies: row, piece
-            constexpr int CPR = ROWB / 16, NCP = (kHalf * CPR + 255) / 256;
-            int cr[NCP], cpc[NCP];
-#pragma unroll
-            for (int i = 0; i < NCP; ++i) {
-                cr[i] = (ut + 256 * i) / CPR;
-                cpc[i] = (ut + 256 * i) % CPR;
-            }
+            // Keys and values have their own warps, which meet only at the raw rows, three steps deep.
+            const bool isv = warp >= 12;
+            const int ut = (tid - 256) & 127, part = ut >> 6, tok = ut & 63;
+            constexpr int ROWB = SH::ROWB;
             const int steps = 2 * nt;
-            // cache offset of token i of step h, or -1
-            auto page_of = [&](int h) -> int {
-                if (h >= steps || ut >= kHalf) return -1;
-                const long long n = (long long)a * kKeys + h * kHalf + ut;
-                if (n >= lim) return -1;
-                const long long s = paged_slot(p.kv, g0 + grp, n);
-                return s < 0 ? -1 : __ldg(p.kv.page_table + s);
-            };
-            auto put_rows = [&](int h, int pid) {
-                if (ut < kHalf) {
-                    const long long n = (long long)a * kKeys + h * kHalf + ut;
-                    long long off = -1;
-                    if (h < steps && n < lim) {
-                        off = paged_row(p.kv, pid, g, n);
-                        if (off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
-                    }
-                    sh.rowoff[h & 3][ut] = off;
-                }
-            };
-            auto fetch = [&](int h) {                  // raw rows of step h; rows that do not exist become zero
-                if (h < steps) {
-                    uint8_t* dst = sh.raw[h % 3];
-#pragma unroll
-                    for (int i = 0; i < NCP; ++i)
-                        if (cr[i] < kHalf) {
-                            const long long off = sh.rowoff[h & 3][cr[i]];
-                            cp_async16(smem_u32(dst + (ut + 256 * i) * 16), p.kv.data + (off >= 0 ? off + cpc[i] * 16 : 0),
-                                       off >= 0);
-                        }
-                }
-                cp_async_commit();
-            };
-            auto sync = [&](bool v) -> bool {          // the 256 threads; the OR of v
-                uint32_t r;
-                asm volatile(
-                    "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 2, 256, p;\n selp.u32 %0, 1, 0, "
-                    "q;\n}\n"
-                    : "=r"(r)
-                    : "r"(uint32_t(v))
-                    : "memory");
-                return r != 0;
-            };
-            for (int h = 0; h < 3; ++h) put_rows(h, page_of(h));
-            int pid = page_of(3);
-            bool stop = sync(false), ok = true;
-            fetch(0);
-            fetch(1);
             for (int h = 0; h < steps; ++h) {
                 const uint32_t T = base + uint32_t(h >> 1);        // tile over the kernel
                 const int stage = T & 1, half = h & 1;
-                cp_async_wait_group<1>();
-                stop = sync(!ok);                      // raw(h) has landed; rows of step h + 2 are known
-                if (stop) break;
-                fetch(h + 2);
-                put_rows(h + 3, pid);
-                pid = page_of(h + 4);
-                const uint8_t* raw = sh.raw[h % 3];
-                // powers of two: the largest scale of the 64 tokens to [2^15, 2^16)
-                uint32_t kmx = 0, vmx = 0;
-                auto top = [](uint32_t w) -> uint32_t {   // larger of two bf16 that are numbers, its bits
-                    const uint32_t lo = w & 0x7fffu, hi = (w >> 16) & 0x7fffu;
-                    return max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u);
-                };
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 s = *reinterpret_cast<const uint4*>(raw + (lane + 32 * i) * ROWB + D);
-                    kmx = max(kmx, max(top(s.x), top(s.y)));
-                    vmx = max(vmx, max(top(s.z), top(s.w)));
+                const uint32_t S = base_raw + uint32_t(h), slot = S % 3;
+                if (!__all_sync(0xffffffffu, wait(&sh.raw_full[slot], (S / 3) & 1))) break;
+                const uint8_t* raw = sh.raw[slot];
+                // powers of two: the largest scale (that is a number) of the 64 tokens to [2^15, 2^16)
+                auto top = [](uint32_t w) -> uint32_t { return max(w & 0x7fffu, (w >> 16) & 0x7fffu); };   // of two bf16
+                uint32_t kmx, vmx;
+                {
+                    const uint4 s0 = *reinterpret_cast<const uint4*>(raw + lane * ROWB + D);
+                    const uint4 s1 = *reinterpret_cast<const uint4*>(raw + (lane + 32) * ROWB + D);
+                    kmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.x, s0.y), max_bf16x2(s1.x, s1.y)), 0u));
+                    vmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.z, s0.w), max_bf16x2(s1.z, s1.w)), 0u));
+                    if (isv) kmx = 0;                      // (only the first key warp needs both)
+                    else if (warp != 8) vmx = 0;
                 }
-                auto expo = [](uint32_t m) { return max(int(m >> 7) - 127, -70) - 15; };
+                auto expo = [](uint32_t m) { return min(max(int(m >> 7) - 127, -70), 127) - 15; };
                 const uint8_t* row = raw + tok * ROWB;
                 const uint4 all = *reinterpret_cast<const uint4*>(row + D);
                 // A tile that some queries do not see whole: every token has its own powers of two, so that what a
@@ -382,16 +378,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 const bool edge = (a + (h >> 1) + 1) * kKeys > lim0;
                 int ek, ev;
                 if (edge) {
-                    ek = expo(max(top(all.x), top(all.y)));
-                    ev = expo(max(top(all.z), top(all.w)));
-                    if (uw < 2) {
+                    ek = expo(top(max_bf16x2(max_bf16x2(all.x, all.y), 0u)));
+                    ev = expo(top(max_bf16x2(max_bf16x2(all.z, all.w), 0u)));
+                    if (!isv && part == 0) {
                         sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
                         sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
                     }
                 } else {
-                    ek = expo(__reduce_max_sync(0xffffffffu, kmx));
-                    ev = expo(__reduce_max_sync(0xffffffffu, vmx));
-                    if (ut == 0) {
+                    ek = isv ? 0 : expo(__reduce_max_sync(0xffffffffu, kmx));
+                    ev = isv || warp == 8 ? expo(__reduce_max_sync(0xffffffffu, vmx)) : 0;
+                    if (!isv && ut == 0) {
                         sh.ek[T & 3][half] = ek;
                         sh.ev[T & 3][half] = ev;
                     }
@@ -400,26 +396,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 const float mul = pow2i(isv ? -ev : -ek);
                 float f[4] = {bf_lo(sc.x) * mul, bf_hi(sc.x) * mul, bf_lo(sc.y) * mul, bf_hi(sc.y) * mul};
                 const int r = half * kHalf + tok;      // row of the operand tile
-                if (isv) {
+                if (isv && edge) {
                     // Tokens that some of the unit's queries do not see: a group that is not finite is taken as 0
                     // (0 * NaN would reach every query) and noted for those that do see it.
                     const int n = (a + (h >> 1)) * kKeys + r;
 #pragma unroll
                     for (int gr = 0; gr < 4; ++gr) {
-                        const bool nan = edge && n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
+                        const bool nan = n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
                         const uint32_t m = __ballot_sync(0xffffffffu, nan);
                         if (lane == 0 && part == 0) sh.poison[T & 3][gr][r >> 5] = m;
                         if (nan) f[gr] = 0.f;
                     }
                 }
-                if (uw < 2) {
-                    const uint32_t m = __ballot_sync(0xffffffffu, sh.rowoff[h & 3][tok] >= 0);
-                    if (lane == 0) sh.valid[T & 3][r >> 5] = m;
-                }
+                if (!isv && part == 0 && lane == 0) sh.valid[T & 3][r >> 5] = sh.raw_valid[slot][tok >> 5];
                 if (half == 0 && T >= 2) {             // the tile two back has been read
-                    ok = __all_sync(0xffffffffu,
-                                    wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1));
-                    if (!ok) continue;                 // (all leave at the next step's barrier)
+                    if (!__all_sync(0xffffffffu,
+                                    wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1)))
+                        break;
                 }
                 uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
                 const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
@@ -466,57 +459,142 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 }
                 fence_async_smem();
                 __syncwarp();
-                if (lane == 0) arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
+                if (lane == 0) {
+                    arrive(&sh.raw_empty[slot]);
+                    arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
+                }
             }
-            cp_async_wait_group<0>();
-        } else if (warp == 8 + kUnpack) {
+        } else if (warp == 8 + kUnpack || warp == 8 + kUnpack + 1) {
             // ================================================================ MMA issue
-            if (lane == 0) {
-                constexpr uint32_t kIdS = idesc_f16(128, kKeys, false);
-                constexpr uint32_t kIdO = idesc_f16(128, D, true);
-                auto s_mma = [&](int i, uint32_t T) {
-                    const uint64_t dq = sw128_desc(smem_u32(sh.q[i]), 16, 1024);
-                    const uint64_t dk = sw128_desc(smem_u32(sh.k[T & 1]), 16, 1024);
+            // A warp per row tile, so that neither waits for the other's weights (one warp for both: 696 us, see the file's
+            // table).  The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.
+            constexpr uint32_t kIdS = idesc_f16(128, kKeys, false);
+            constexpr uint32_t kIdO = idesc_f16(128, D, true);
+            const uint64_t dq0 = sw128_desc(smem_u32(sh.q[0]), 16, 1024);
+            const uint64_t dk0 = sw128_desc(smem_u32(sh.k[0]), 16, 1024);
+            const uint64_t dv0 = sw128_desc(smem_u32(sh.v[0]), kSlab, 1024);
+            constexpr uint64_t kTile16 = SH::kTile >> 4;       // a stage's or row tile's step in a descriptor
+            // S of row tile i against a tile's keys; O += P V over 64 tokens
+            const int i = warp - (8 + kUnpack);
+            const bool solo = ntile == 1;              // row tile 0 stands for both
+            const bool part = i < ntile;
+            const bool leader = elect_one();           // one thread issues and commits: a commit tracks its own thread's MMAs
+            auto s_mma = [&](uint32_t T) {
+                const uint64_t dq = dq0 + uint32_t(i) * kTile16;
+                const uint64_t dk = dk0 + (T & 1) * kTile16;
+                const uint32_t dst = tmem + i * 128;
+                if (leader) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint64_t off = uint64_t(((kk >> 2) * kSlab + (kk & 3) * 32) >> 4);
-                        umma_bf16(tmem + i * 128, dq + off, dk + off, kIdS, kk > 0);
+                        umma_bf16(dst, dq + off, dk + off, kIdS, kk > 0);
                     }
                     umma_commit(&sh.s_full[i]);
-                };
-                auto pv_mma = [&](int i, uint32_t T, bool first) {
-                    const uint64_t dv = sw128_desc(smem_u32(sh.v[T & 1]), kSlab, 1024);
+                }
+                __syncwarp();
+            };
+            auto pv_mma = [&](uint32_t T, int h, bool first) {
+                const uint64_t dv = dv0 + (T & 1) * kTile16 + uint64_t(h * ((kHalf * 128) >> 4));
+                const uint32_t src = tmem + i * 128 + h * 64, dst = tmem + 256 + i * 128;
+                const uint32_t acc0 = !first || h > 0 ? 1u : 0u;
+                if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        umma_ts(tmem + 256 + i * 128, tmem + i * 128 + kk * 8, dv + uint64_t((kk * 2048) >> 4), kIdO,
-                                (!first || kk > 0) ? 1u : 0u);
-                };
-                bool live = wait(&sh.q_full, segs & 1) && wait(&sh.k_full[base & 1], (base >> 1) & 1);
-                if (live) {
+                    for (int kk = 0; kk < kHalf / 16; ++kk)
+                        umma_ts(dst, src + kk * 8, dv + uint64_t((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : acc0);
+                    if (h == 0) umma_commit(&sh.pv_half[i]);
+                }
+                __syncwarp();
+            };
+            auto commit = [&](uint64_t* bar) {
+                if (leader) {
+                    umma_commit(bar);
+                    if (solo) umma_commit(bar);
+                }
+                __syncwarp();
+            };
+            auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
+            bool live = part && all(wait(&sh.q_full, segs & 1)) && all(wait(&sh.k_full[base & 1], (base >> 1) & 1));
+            if (live) {
+                tc_fence_after();
+                s_mma(base);
+                commit(&sh.k_empty[base & 1]);
+            }
+            // Half by half: O takes the first half's weights while the softmax is at the second.  (Logits by halves too,
+            // N = 64, so that the next tile's begin as early, take half as many products again, about 73 clocks each at
+            // either width: slower.)
+            for (int t = 0; live && t < nt; ++t) {
+                const uint32_t T = base + uint32_t(t);
+                live = all(wait(&sh.v_full[T & 1], (T >> 1) & 1));
+                for (int h = 0; live && h < 2; ++h) {
+                    live = all(wait(&sh.p_full[i][h], ((i ? base1 : base) + uint32_t(t)) & 1));
+                    if (!live) break;
                     tc_fence_after();
-                    for (int i = 0; i < ntile; ++i) s_mma(i, base);
-                    umma_commit(&sh.k_empty[base & 1]);
+                    pv_mma(T, h, t == 0);
                 }
-                for (int t = 0; live && t < nt; ++t) {
-                    const uint32_t T = base + uint32_t(t);
-                    live = wait(&sh.v_full[T & 1], (T >> 1) & 1);
-                    for (int i = 0; live && i < ntile; ++i) {
-                        live = wait(&sh.p_full[i], ((i ? base1 : base) + uint32_t(t)) & 1);
-                        if (!live) break;
-                        tc_fence_after();
-                        pv_mma(i, T, t == 0);
-                        if (i == ntile - 1) umma_commit(&sh.v_empty[T & 1]);
-                        if (t + 1 < nt) {
-                            if (i == 0) live = wait(&sh.k_full[(T + 1) & 1], ((T + 1) >> 1) & 1);
-                            if (!live) break;
-                            tc_fence_after();
-                            s_mma(i, T + 1);
-                            if (i == ntile - 1) umma_commit(&sh.k_empty[(T + 1) & 1]);
-                        }
-                    }
+                if (!live) break;
+                commit(&sh.v_empty[T & 1]);
+                if (t + 1 < nt) {
+                    live = all(wait(&sh.k_full[(T + 1) & 1], ((T + 1) >> 1) & 1));
+                    if (!live) break;
+                    tc_fence_after();
+                    s_mma(T + 1);
+                    commit(&sh.k_empty[(T + 1) & 1]);
                 }
-                umma_commit(&sh.o_done);
-                if (!live) wait(&sh.o_done, segs & 1);   // what was issued before a wait gave up
+            }
+            if (part) commit(&sh.o_done);
+            if (part && !live) wait(&sh.o_done, segs & 1);   // what was issued before a wait gave up
+            __syncwarp();
+        } else if (warp == 8 + kUnpack + 2) {
+            // ================================================================ raw rows
+            constexpr int ROWB = SH::ROWB;
+            const int rsh = min(6, p.kv.page_shift), R = 1 << rsh, runs = kHalf >> rsh;   // runs of R tokens per step
+            const int32_t* const pt = p.kv.page_table + (long long)(g0 + grp) * p.kv.max_pages;
+            const int steps = 2 * nt;
+            // page of this lane's run of step h (lim <= len: inside the table)
+            auto page_of = [&](int h) -> int {
+                const int n = a * kKeys + h * kHalf + lane * R;
+                return h < steps && lane < runs && n < lim ? __ldg(pt + (n >> p.kv.page_shift)) : -1;
+            };
+            int pid = page_of(0);
+            for (int h = 0; h < steps; ++h) {
+                const uint32_t S = base_raw + uint32_t(h), slot = S % 3;
+                const int n = a * kKeys + h * kHalf + lane * R;
+                int rows = lane < runs ? min(max(lim - n, 0), R) : 0;
+                const long long off = rows > 0 ? paged_row(p.kv, pid, g, n) : -1;
+                if (rows > 0 && off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+                if (off < 0) rows = 0;
+                pid = page_of(h + 1);
+                if (S >= 3 && !__all_sync(0xffffffffu, wait(&sh.raw_empty[slot], (S / 3 - 1) & 1))) break;
+                const uint32_t dst = smem_u32(sh.raw[slot]) + lane * R * ROWB;
+                uint32_t m0 = 0, m1 = 0;               // this lane's tokens among the step's 64
+                if (rows > 0) {
+                    const unsigned long long m = (rows >= 64 ? ~0ull : (1ull << rows) - 1) << (lane * R & 63);
+                    m0 = uint32_t(m);
+                    m1 = uint32_t(m >> 32);
+                }
+                m0 = __reduce_or_sync(0xffffffffu, m0);
+                m1 = __reduce_or_sync(0xffffffffu, m1);
+                if ((m0 & m1) != 0xffffffffu && lane < runs) {   // tokens that do not exist: scales of zero
+                    for (int i = rows; i < R; ++i)
+                        *reinterpret_cast<uint4*>(sh.raw[slot] + (lane * R + i) * ROWB + D) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                }
+                if (lane == 0) {
+                    sh.raw_valid[slot][0] = m0;
+                    sh.raw_valid[slot][1] = m1;
+                }
+                __syncwarp();                          // the zeros and the masks before the arrival
+                if (lane == 0)
+                    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n" ::"r"(
+                                     smem_u32(&sh.raw_full[slot])),
+                                 "r"(uint32_t((__popc(m0) + __popc(m1)) * ROWB))
+                                 : "memory");
+                __syncwarp();
+                if (rows > 0)
+                    asm volatile(
+                        "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(dst),
+                        "l"(p.kv.data + off), "r"(uint32_t(rows * ROWB)), "r"(smem_u32(&sh.raw_full[slot]))
+                        : "memory");
             }
             __syncwarp();
         } else if (warp < 8) {
@@ -594,7 +672,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 ok = __all_sync(0xffffffffu, wait(&sh.s_full[rt], Ti & 1));
                 if (!ok) break;
                 tc_fence_after();
-                if (t > 0) poisoned(t - 1);
                 const int n0 = n0_of(t);
                 const uint4 vd = *reinterpret_cast<const uint4*>(sh.valid[T & 3]);
                 const uint32_t vm[4] = {vd.x, vd.y, vd.z, vd.w};
@@ -624,25 +701,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         }
                     }
                 };
-                // (the loops over 32 columns are not unrolled: the warps' roles share the instruction cache)
-                float top = -INFINITY;
-#pragma unroll 1
-                for (int q4 = 0; q4 < 4; ++q4) {
-                    float v[32];
-                    tmem_ld32(t_s + q4 * 32, v);
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-                    if (edge || gaps) masked(q4, v);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
-                    const float x4 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    top = fmaxf(top, edge || gaps ? x4 : fmaf(x4, q4 < 2 ? cs[0] : cs[1], q4 < 2 ? ev[0] : ev[1]));
-                }
-                if (__any_sync(0xffffffffu, top > m + kSlack)) {
+                // The reference of the warp's rows up to `top` where that exceeds it by 2^kSlack, with l and O.  What has
+                // been issued into O is complete before: of the tile before, shown by S(t); at the second half, this
+                // tile's first.
+                auto follow = [&](float top, int h) {
+                    if (h == 1) {
+                        ok = __all_sync(0xffffffffu, wait(&sh.pv_half[rt], Ti & 1)) && ok;
+                        tc_fence_after();
+                    }
                     const float mn = top > m + kSlack ? top : m;
                     const float f = mn == -INFINITY ? 1.f : ex2_approx(m - mn);
                     m = mn;
                     l *= f;
-                    if (t > 0) {                           // S(t) complete: so is P(t - 1) V
+                    if (t > 0 || h == 1) {
 #pragma unroll 1
                         for (int c = 0; c < D; c += 32) {
                             float v[32];
@@ -651,10 +722,35 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                             for (int i = 0; i < 32; ++i) v[i] *= f;
                             tmem_st32(t_o + c, v);
                         }
+                        tmem_wait_st();
                     }
-                }
-                const float ref = m == -INFINITY ? 0.f : kBase - m;
+                };
+                auto done = [&](int h) {               // the weights of a half are stored
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(&sh.p_full[rt][h]);
+                };
+                // (the loops over 32 columns are not unrolled: the warps' roles share the instruction cache)
+                auto top_of = [&](int q0, int q1) -> float {
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int q4 = q0; q4 < q1; ++q4) {
+                        float v[32];
+                        tmem_ld32(t_s + q4 * 32, v);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        if (edge || gaps) masked(q4, v);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], v[i]);
+                        const float x4 = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        top = fmaxf(top, edge || gaps ? x4 : fmaf(x4, q4 < 2 ? cs[0] : cs[1], q4 < 2 ? ev[0] : ev[1]));
+                    }
+                    return top;
+                };
                 if (edge || gaps) {
+                    if (t > 0) poisoned(t - 1);
+                    const float top = top_of(0, 4);
+                    if (__any_sync(0xffffffffu, top > m + kSlack)) follow(top, 0);
+                    const float ref = m == -INFINITY ? 0.f : kBase - m;
 #pragma unroll 1
                     for (int q4 = 0; q4 < 4; ++q4) {
                         float v[32];
@@ -669,31 +765,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-                        tmem_st16(t_s + q4 * 16, o);
+                        tmem_st16(t_s + (q4 >> 1) * 64 + (q4 & 1) * 16, o);
                     }
+                    done(0);
+                    done(1);
                 } else {
+                    // One pass: the weights of 64 columns are computed for the reference as it is; only if one of them
+                    // reaches 2^15 (in fp16: none is lost as long as it is below 2^16) is the maximum looked for, the
+                    // reference moved and the half done again.  A row without a reference starts with the maximum.
+                    if (__any_sync(0xffffffffu, m == -INFINITY)) {
+                        const float top = top_of(0, 2);
+                        if (__any_sync(0xffffffffu, top > m + kSlack)) follow(top, 0);
+                    }
 #pragma unroll 1
-                    for (int q4 = 0; q4 < 4; ++q4) {
-                        const float c = q4 < 2 ? cs[0] : cs[1], e = q4 < 2 ? ev[0] : ev[1], off = e + ref;
-                        float sum[2] = {0.f, 0.f};
-                        float v[32];
-                        tmem_ld32(t_s + q4 * 32, v);
-                        uint32_t o[16];
+                    for (int h = 0; h < 2; ++h) {
+                        const float c = h ? cs[1] : cs[0], e = h ? ev[1] : ev[0];
+                        uint32_t o[2][16];
+                        float sum[2];
+#pragma unroll 1
+                        for (int turn = 0;; ++turn) {
+                            const float off = e + (m == -INFINITY ? 0.f : kBase - m);
+                            uint32_t hm = 0;
+                            sum[0] = sum[1] = 0.f;
+                            // 16 columns at a time, the next ones on their way
+                            float v[2][16];
+                            ld16_begin(t_s + h * 64, v[0]);
+                            ld_wait(v[0]);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            v[2 * i] = ex2_approx(fmaf(v[2 * i], c, off));
-                            v[2 * i + 1] = ex2_approx(fmaf(v[2 * i + 1], c, off));
-                            o[i] = pack_f16(v[2 * i], v[2 * i + 1]);
-                            sum[0] += v[2 * i];
-                            sum[1] += v[2 * i + 1];
+                            for (int q = 0; q < 4; ++q) {
+                                float (&x)[16] = v[q & 1];
+                                if (q < 3) ld16_begin(t_s + h * 64 + (q + 1) * 16, v[(q + 1) & 1]);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    ffma2(x[2 * i], x[2 * i + 1], c, off);
+                                    x[2 * i] = ex2_approx(x[2 * i]);
+                                    x[2 * i + 1] = ex2_approx(x[2 * i + 1]);
+                                    uint32_t& w = o[q >> 1][(q & 1) * 8 + i];
+                                    w = pack_f16(x[2 * i], x[2 * i + 1]);
+                                    hm = max_f16x2(hm, w);
+                                    fadd2(sum[0], sum[1], x[2 * i], x[2 * i + 1]);
+                                }
+                                if (q < 3) ld_wait(v[(q + 1) & 1]);
+                            }
+                            const bool over = (hm & 0x7fffu) >= 0x7800u || (hm >> 16) >= 0x7800u;
+                            if (turn || !__any_sync(0xffffffffu, over)) break;
+                            follow(top_of(2 * h, 2 * h + 2), h);
                         }
-                        tmem_st16(t_s + q4 * 16, o);
+                        tmem_st16(t_s + h * 64, o[0]);
+                        tmem_st16(t_s + h * 64 + 16, o[1]);
                         l = fmaf(sum[0] + sum[1], ex2_approx(-e), l);
+                        done(h);
                     }
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(&sh.p_full[rt]);
             }
 
             // ---- output, or a share of a split unit
@@ -815,16 +938,23 @@ void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch) {
 spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st) {
     const int sms = device_info().num_sms;
     const int TQ = paged_tokens_per_tile(256, p.Hq / p.kv.Hkv);
-    for (int g0 = 0; g0 < p.kv.B; g0 += kPagedMaxUnits) {
-        const int groups = p.kv.B - g0 < kPagedMaxUnits ? p.kv.B - g0 : kPagedMaxUnits;
+    // the prefix of a launch's sequences lies in shared memory, in 32 bits: a sequence's query tiles times its
+    // tiles bound its part
+    const long long tiles = (((long long)p.kv.max_pages << p.kv.page_shift) + kKeys - 1) / kKeys + kSegC;
+    const long long most = tiles * p.kv.Hkv * (((long long)p.T + TQ - 1) / TQ);
+    long long step = kChunkUnits;
+    if (most + tiles * p.kv.Hkv * step > 0xffffffffll) step = (0xffffffffll - most) / (tiles * p.kv.Hkv);
+    if (step < 1) return SPA_ERR_UNSUPPORTED_SHAPE;
+    for (int g0 = 0; g0 < p.kv.B; g0 += int(step)) {
+        const int groups = p.kv.B - g0 < step ? p.kv.B - g0 : int(step);
 #define SPA_PC(DD)                                                                                              \
     if (p.kv.d == DD) {                                                                                         \
-        constexpr size_t kMost = sizeof(ChunkShared<DD>) + size_t(kPagedMaxUnits + 1) * 8;                       \
+        constexpr size_t kMost = sizeof(ChunkShared<DD>) + size_t(kChunkUnits + 1) * 4;                          \
         static_assert(kMost <= 227 * 1024, "paged chunk: shared memory over the per-CTA limit");                 \
         SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_chunk_kernel<DD>),                        \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)));                   \
         SPA_CUDA_TRY(launch_pdl(paged_chunk_kernel<DD>, dim3(sms), dim3(kThreads),                               \
-                                sizeof(ChunkShared<DD>) + size_t(groups + 1) * 8, st, p, g0, groups, TQ));        \
+                                sizeof(ChunkShared<DD>) + size_t(groups + 1) * 4, st, p, g0, groups, TQ));        \
     }
         SPA_PC(64) SPA_PC(128)
 #undef SPA_PC
