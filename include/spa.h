@@ -553,7 +553,8 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
 
 /* Exact softmax attention of the new tokens over the cache: out[t][h] = softmax(sm_scale q K^T) V.
  *   idx NULL: the i-th of sequence b's n new tokens sees tokens [0, kv_len[b] - n + i] (causal).
- *   idx, count: one query per sequence (T = B, seq_start NULL), restricted to supports as
+ *   idx, count: at most one query per sequence (T <= B; seq_start NULL, or one or no new token
+ *   each, more of them raise the status word's bit), restricted to supports as
  *   spa_sparse_attend takes them: [U, cap] and [U], entry e covers tokens [e * unit_tokens,
  *   (e + 1) * unit_tokens) below kv_len[b]; U = B * Hkv (collapse GROUP_MEAN) or B * Hq (NONE).
  *   q [T, Hq, d] bf16 with token and head strides (elements, multiples of 8), 16-byte aligned;

@@ -654,7 +654,7 @@ def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     """Exact softmax attention of the new tokens over a paged cache (bf16 or 4-bit); see spa_paged_attend in
     include/spa.h.  q [T, Hq, d] bf16.  Whole cache: every query sees the tokens up to its own; seq_start
     [B + 1] int32 groups several queries per sequence.  Supports: idx [U, cap], count [U] int32 as select_topk
-    and select_topp give them, one query per sequence.  plan.out [T, Hq, d] bf16, plan.out_f32, plan.lse [T, Hq]."""
+    and select_topp give them, at most one query per sequence.  plan.out [T, Hq, d] bf16, plan.out_f32, plan.lse [T, Hq]."""
     kv = _paged_kv(cache, page_table, kv_len)
     _rows(q, "q", None, kv.d)
     T, Hq, d = q.shape
@@ -666,8 +666,8 @@ def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     a.seq_start, a.q, a.q_token_stride, a.q_head_stride = _ptr(seq_start), _ptr(q), q.stride(0), q.stride(1)
     a.collapse, a.unit_tokens = collapse, unit_tokens
     if idx is not None:
-        if seq_start is not None:
-            raise ValueError("supports take one query per sequence, without seq_start")
+        if T > kv.B:
+            raise ValueError(f"supports take at most one query per sequence: got {T} for {kv.B} sequences")
         U = kv.B * (kv.Hkv if collapse == SPA_COLLAPSE_GROUP_MEAN else Hq)
         _need(idx, torch.int32, "idx")
         _need(count, torch.int32, "count")

@@ -147,7 +147,7 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     if (a->Hq / a->kv.Hkv > 16) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(a->out) || !aligned16(a->out_f32) || !aligned16(ws)) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (a->idx) {
-        if (a->seq_start || a->cap < 0 || a->unit_tokens <= 0) return SPA_ERR_INVALID_ARG;
+        if (a->T > a->kv.B || a->cap < 0 || a->unit_tokens <= 0) return SPA_ERR_INVALID_ARG;
         if (a->collapse != SPA_COLLAPSE_NONE && a->collapse != SPA_COLLAPSE_GROUP_MEAN) return SPA_ERR_INVALID_ARG;
     }
     if (ws_bytes < spa_paged_attend_workspace_bytes(a)) return SPA_ERR_WORKSPACE_TOO_SMALL;

@@ -171,7 +171,18 @@ __device__ __forceinline__ SeqGeo seq_geo(const PagedAttendParams& p, int b, boo
     return s;
 }
 
-__device__ __forceinline__ int support_tokens(const PagedAttendParams& p, int u) {
+// Query row of a sequence's one new token, or -1: it has none, or (an error with supports) several.
+__device__ __forceinline__ int one_row(const PagedAttendParams& p, int b, bool* bad) {
+    if (!p.seq_start) return b;
+    const int a = p.seq_start[b], e = p.seq_start[b + 1];
+    if (a >= 0 && e <= p.T && (long long)e - a == 1) return a;
+    if (e != a) *bad = true;
+    return -1;
+}
+
+// tokens that support u names, or -1: its sequence has no query
+__device__ __forceinline__ int support_tokens(const PagedAttendParams& p, int u, bool* bad) {
+    if (one_row(p, u / (p.collapse == SPA_COLLAPSE_GROUP_MEAN ? p.kv.Hkv : p.Hq), bad) < 0) return -1;
     int c = p.count[u];
     c = c < 0 ? 0 : c > p.cap ? p.cap : c;
     const long long n = (long long)c * p.unit_tokens;
@@ -229,9 +240,11 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
         long long t = 0;
         if (u < groups) {
             if (sparse) {
-                const int n = support_tokens(p, g0 + u);
+                bool bad = false;
+                const int n = support_tokens(p, g0 + u, &bad);
                 t = n > 0 ? (n + TILE - 1) / TILE + kSeg : 0;
                 empties |= n == 0;
+                if (bad && blockIdx.x == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
             } else {
                 bool bad = false;
                 const SeqGeo s = seq_geo(p, g0 + u, &bad);
@@ -281,7 +294,9 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
             if (s_prefix[u + 1] != s_prefix[u]) continue;
             const bool grp = p.collapse == SPA_COLLAPSE_GROUP_MEAN;
             const int per = grp ? p.kv.Hkv : p.Hq;
-            write_empty((g0 + u) / per, 1, ((g0 + u) % per) * (grp ? G : 1), grp ? G : 1);
+            bool bad = false;
+            const int row = one_row(p, (g0 + u) / per, &bad);
+            if (row >= 0) write_empty(row, 1, ((g0 + u) % per) * (grp ? G : 1), grp ? G : 1);
         } else {
             bool bad = false;
             const SeqGeo s = seq_geo(p, g0 + u, &bad);
@@ -324,12 +339,12 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
             un.g = gm ? r : r / G;
             un.h0 = gm ? r * G : r;
             un.heads = gm ? G : 1;
-            un.row0 = un.b;
+            un.row0 = one_row(p, un.b, &bad);
             un.nq = 1;
             un.len = paged_len(p.kv, p.kv.kv_len[un.b], &bad);
             un.lim0 = un.len;
             un.u = g0 + grp;
-            un.ntok = support_tokens(p, g0 + grp);
+            un.ntok = support_tokens(p, g0 + grp, &bad);
             u_lo = s_prefix[grp];
             tiles = (un.ntok + TILE - 1) / TILE;
         } else {
@@ -1118,7 +1133,7 @@ spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
     const int sms = device_info().num_sms;
     const bool sparse = p.idx != nullptr;
     const int heads = sparse && p.collapse == SPA_COLLAPSE_NONE ? 1 : G;
-    const long long all = !sparse ? p.kv.B : (long long)p.T * (p.collapse == SPA_COLLAPSE_GROUP_MEAN ? p.kv.Hkv : p.Hq);
+    const long long all = !sparse ? p.kv.B : (long long)p.kv.B * (p.collapse == SPA_COLLAPSE_GROUP_MEAN ? p.kv.Hkv : p.Hq);
     int nt, TQ;
     paged_shape(p.T, p.kv.B, heads, sparse, &nt, &TQ);
     // the prefix of a launch's groups lies in shared memory, so a launch takes at most kPagedMaxUnits of them

@@ -513,7 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 __syncwarp();
             };
             auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
-            bool live = part && all(wait(&sh.q_full, segs & 1)) && all(wait(&sh.k_full[base & 1], (base >> 1) & 1));
+            // (a warp without a row tile waits for the queries all the same: it must not run ahead of a phase)
+            bool live = all(wait(&sh.q_full, segs & 1)) && part && all(wait(&sh.k_full[base & 1], (base >> 1) & 1));
             if (live) {
                 tc_fence_after();
                 s_mma(base);

@@ -354,6 +354,30 @@ def test_attend_a_chunk(fmt, d, Hkv, G, page, new, lens):
     assert torch.equal(first, plan.out)
 
 
+def test_units_of_one_and_two_row_tiles_in_turn():
+    # a CTA takes units of up to 128 rows and of more in turn, more of them than there are SMs: the second row tile's
+    # warps sit out some units and must neither lag nor run ahead
+    rng = np.random.default_rng(51)
+    new = [int(x) for x in rng.choice([3, 20, 40, 64, 33, 50], 180)]
+    lens = [int(n + x) for n, x in zip(new, rng.integers(0, 700, 180))]
+    c = Cache(lens, 2, 128, 16, INT4, seed=51)
+    start = np.concatenate(([0], np.cumsum(new)))
+    q = torch.randn(int(start[-1]), 8, 128, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32(start), **c.kw)
+    out, lse, qv = _bf(plan.out), _np(plan.lse).astype(np.float64), _bf(q)
+    assert np.isfinite(out).all()
+    for b in range(0, 180, 7):
+        for i in (0, new[b] // 2, new[b] - 1):
+            t = start[b] + i
+            check_attention(c, qv[t], out[t], lse[t], [np.arange(lens[b]) <= lens[b] - new[b] + i] * 2, 0.09, b,
+                            f"sequence {b}, query {i}")
+    first = plan.out.clone()
+    for _ in range(20):
+        plan.run()
+        assert torch.equal(first, plan.out)
+    assert spa.read_device_status(plan.ws) == 0
+
+
 def test_a_long_chunk_is_split_and_merged():
     c = Cache([30_000, 17], 1, 128, 64, INT4, seed=31)
     start = [0, 90, 107]
@@ -469,6 +493,24 @@ def test_attend_supports(fmt, collapse, unit, page, d):
     for b in range(len(lens)):
         s = [x & (lens[b] > 0) for x in sees[b * per:(b + 1) * per]]
         check_attention(c, _bf(q)[b], out[b], lse[b], s, 0.1, b, f"length {lens[b]}")
+
+
+def test_supports_of_a_batch_with_empty_places():
+    # sequences 1 and 3 have no query, sequence 4 (against the rules) two; rows of nobody stay
+    Hkv, G, lens = 2, 2, [40, 30, 50, 0, 20]
+    c = Cache(lens, Hkv, 64, 16, INT4, seed=21)
+    q = torch.randn(5, Hkv * G, 64, device="cuda").to(torch.bfloat16)
+    idx = np.tile(np.arange(6, dtype=np.int32), (5 * Hkv, 1))
+    kw = dict(q=q, sm_scale=0.1, idx=_i32(idx), count=_i32(np.full(5 * Hkv, 6)), unit_tokens=4, **c.kw)
+    for last, status in ((2, 0), (4, INVALID)):
+        plan = spa.paged_attend(seq_start=_i32([0, 1, 1, 2, 2, last]), run=False, **kw)
+        plan.out.fill_(9)
+        plan.run()
+        assert spa.read_device_status(plan.ws) == status
+        out, lse = _bf(plan.out), _np(plan.lse).astype(np.float64)
+        for row, b in ((0, 0), (1, 2)):
+            check_attention(c, _bf(q)[row], out[row], lse[row], [np.arange(lens[b]) < 24] * Hkv, 0.1, b, f"row {row}")
+        assert (out[2:] == 9).all()
 
 
 def test_count_above_cap_is_cut():
@@ -724,7 +766,7 @@ def test_python_refusals():
     with pytest.raises(spa.SpaError):       # q_out over q
         spa.paged_append(k=k, v=k, q=q, q_out=q, **c.kw)
     for bad in (dict(q=q[:1]), dict(idx=_i32([[0]])), dict(idx=_i32([[0]]), count=_i32([1])),
-                dict(seq_start=_i32([0, 1, 2]), idx=_i32(np.zeros((4, 1))), count=_i32(np.zeros(4)))):
+                dict(q=torch.cat([q, q]), seq_start=_i32([0, 1, 4]), idx=_i32(np.zeros((4, 1))), count=_i32(np.zeros(4)))):
         with pytest.raises((TypeError, ValueError)):
             spa.paged_attend(**{**dict(q=q, sm_scale=0.1), **c.kw, **bad})
     with pytest.raises(spa.SpaError):       # 17 query heads per kv head

@@ -205,7 +205,7 @@ def test_small_workspaces_are_refused():
     (dict(idx=256), "INVALID_ARG"), (dict(idx=256, count=256, unit_tokens=0), "INVALID_ARG"),
     (dict(idx=256, count=256, unit_tokens=1, cap=-1), "INVALID_ARG"),
     (dict(idx=256, count=256, unit_tokens=1, collapse=2), "INVALID_ARG"),
-    (dict(idx=256, count=256, unit_tokens=1, seq_start=256), "INVALID_ARG")])
+    (dict(idx=256, count=256, unit_tokens=1, seq_start=256, T=3), "INVALID_ARG")])
 def test_attend_refusals(kw, want):
     t = _abi.SpaPagedAttendArgs(kv=_kv(), **{**dict(T=2, Hq=4, q=256, out=256), **kw})
     assert _call("spa_paged_attend", t) == "SPA_ERR_" + want
