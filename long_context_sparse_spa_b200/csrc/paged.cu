@@ -14,7 +14,11 @@
 // the rotation itself in fp32 without contraction.
 //
 // Each row of d channels is held by d/8 lanes, 8 channels (16 bytes) each; pair partners and group
-// maxima are exchanged by shuffles, so a row is read once and nothing is written before it is read.
+// maxima are exchanged by shuffles, so a row is read once.
+//
+// Measured on B200: append of 4096 tokens (32 query, 8 kv heads, d = 128) in 4 bits about 33 us and 8 us for reading
+// them back, 88 + 22 MB; bound by instruction issue (rotation and quantisation of 16-byte pieces).  Gather of 28672
+// 4-bit tokens of 8 heads to bf16 (150 MB) 28.7 us, 5.2 TB/s, bound by memory and shared memory together.
 #include "paged.cuh"
 
 namespace spa {
