@@ -278,6 +278,11 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
     }
     if (tid == 0) s_prefix[groups] = uint32_t(running);
     empties = __syncthreads_or(empties);
+    // Starts out of order can make sequences overlap, and their tiles more than the host counted and the prefix holds.
+    if (running > 0xffffffffll) {
+        if (blockIdx.x == 0 && tid == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+        running = 0;
+    }
     const long long TT = running;
     const int cta = blockIdx.x;
     // CTAs with work: none gets less than about kShare tiles, since every share of a unit is merged

@@ -267,6 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
     tc_fence_before();
     empties = __syncthreads_or(empties);               // (also: barriers initialised, TMEM allocated)
     tc_fence_after();
+    // Starts out of order can make sequences overlap, and their tiles more than the host counted and the prefix holds.
+    if (running > 0xffffffffll) {
+        if (blockIdx.x == 0 && tid == 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+        running = 0;
+    }
     const long long TT = running;
     const int cta = blockIdx.x;
     const long long shares = (TT + kSegC) / (kSegC + 1);

@@ -741,6 +741,58 @@ def test_two_plans_on_two_streams_do_not_disturb_each_other():
                             b, f"length {L}")
 
 
+def test_chunks_on_two_streams_and_in_a_graph():
+    cs = [Cache([700, 90, 300], 2, d, 16, INT4, seed=s, extra=2) for s, d in ((41, 128), (42, 64))]
+    start = [0, 60, 61, 161]
+    qs = [torch.randn(161, 8, c.d, device="cuda").to(torch.bfloat16) for c in cs]
+    plans = [spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32(start), run=False, **c.kw) for c, q in zip(cs, qs)]
+    plans.append(spa.paged_attend(q=qs[0][:3].contiguous(), sm_scale=0.1, run=False, **cs[0].kw))   # and a decode beside them
+    streams = [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s in zip(plans, streams):
+            p.run(s)
+    torch.cuda.synchronize()
+
+    def check(lens):
+        for c, q, p in zip(cs, qs, plans):
+            assert spa.read_device_status(p.ws) == 0
+            for b in range(3):
+                n = start[b + 1] - start[b]
+                for i in (0, n - 1):
+                    t = start[b] + i
+                    check_attention(c, _bf(q)[t], _bf(p.out)[t], _np(p.lse)[t].astype(np.float64),
+                                    [np.arange(len(c.K[b][0])) <= lens[b] - n + i] * 2, 0.1, b, f"row {t}")
+
+    check([700, 90, 300])
+    check_attention(cs[0], _bf(qs[0])[1], _bf(plans[2].out)[1], _np(plans[2].lse)[1].astype(np.float64),
+                    [np.ones(90, bool)] * 2, 0.1, 1, "decode")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        plans[0].run()
+        plans[1].run()
+    for c in cs:                             # shorter sequences, as if tokens had been taken back
+        c.kw["kv_len"].copy_(_i32([650, 61, 111]))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    check([650, 61, 111])
+
+
+def test_starts_out_of_order_are_reported():
+    # overlapping, negative and too large starts: nothing outside the tensors is touched, the status says so
+    for n, fmt in ((3, INT4), (3, BF16), (200, INT4)):
+        c = Cache([300] * 4, 1, 64, 16, fmt, seed=43)
+        q = torch.randn(n, 4, 64, device="cuda").to(torch.bfloat16)
+        for start in ([0, n, 0, n, 1], [5, 4, 3, 2, 1], [-7, 2, 1 << 30, 2, n], [0, 0, 0, 0, n + 9]):
+            plan = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32(start), **c.kw)
+            assert spa.read_device_status(plan.ws) == INVALID
+            add = spa.paged_append(k=q[:, :1], v=q[:, 1:2], q=q, seq_start=_i32(start), **c.kw)
+            assert spa.read_device_status(add.ws) in (0, INVALID)
+        good = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32([0, 1, 1, 2, n]), **c.kw)
+        assert spa.read_device_status(good.ws) == 0
+
+
 def test_a_plan_built_on_one_stream_runs_on_another_at_once():
     c = Cache([500], 1, 128, 16, INT4, seed=13)
     s = torch.cuda.Stream()
