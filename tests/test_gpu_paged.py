@@ -641,6 +641,49 @@ def test_many_sequences_and_supports_pass_one_launch():
         check_attention(c, qv[b], out[b], lse[b], [np.arange(lens[b]) < 8] * 2, 0.2, b, f"supports of {b}")
 
 
+def test_chunks_of_many_sequences_pass_one_launch():
+    B, n = 600, 18                           # 36 rows of each sequence and kv head; some have none of them
+    lens = [n + (7 * b) % 150 for b in range(B)]
+    news = [n if b % 5 else 0 for b in range(B)]
+    news[256] = news[255] = news[512] = 29
+    lens[256] = 29
+    lens[255] = lens[512] = 160
+    start = np.concatenate(([0], np.cumsum(news)))
+    c = Cache(lens, 1, 64, 16, INT4, seed=51)
+    T = int(start[-1]) + 300 * n             # (rows behind the last sequence count towards the choice of a kernel)
+    q = torch.randn(T, 2, 64, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.2, seq_start=_i32(start), run=False, **c.kw)
+    plan.out.fill_(9)
+    plan.run()
+    assert spa.read_device_status(plan.ws) == 0
+    out, lse, qv = _bf(plan.out), _np(plan.lse).astype(np.float64), _bf(q)
+    assert (out[start[-1]:] == 9).all()
+    for b in list(range(1, B, 61)) + [255, 256, 257, 511, 512, 513, B - 1]:
+        for i in range(news[b]):
+            t = start[b] + i
+            check_attention(c, qv[t], out[t], lse[t], [np.arange(lens[b]) <= lens[b] - news[b] + i], 0.2, b,
+                            f"sequence {b}, query {i}")
+
+
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [60, 45]])
+def test_scales_of_the_softmax_that_are_not_positive(fmt, new):
+    lens = [90, 700]
+    c = Cache(lens, 2, 128, 16, fmt, seed=52)
+    start = np.concatenate(([0], np.cumsum(new)))
+    q = torch.randn(int(start[-1]), 8, 128, device="cuda").to(torch.bfloat16)
+    for scale in (-0.1, 0.0):
+        plan = spa.paged_attend(q=q, sm_scale=scale, seq_start=_i32(start), **c.kw)
+        assert spa.read_device_status(plan.ws) == 0
+        out, lse = _bf(plan.out), _np(plan.lse).astype(np.float64)
+        for b, (n, L) in enumerate(zip(new, lens)):
+            for i in sorted({0, n // 2, n - 1}):
+                t = start[b] + i
+                # softmax(-s q K) is softmax(s (-q) K)
+                check_attention(c, -_bf(q)[t], out[t], lse[t], [np.arange(L) <= L - n + i] * 2, -scale, b,
+                                f"scale {scale}, sequence {b}, query {i}")
+
+
 # ------------------------------------------------------------------------------------------------ as used
 def test_decode_loop_in_a_graph_matches_the_oracle():
     """Prompt, then decode steps replayed from one graph: append with rotation, then attention; kv_len on the
