@@ -120,7 +120,7 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
 }
 
 static bool chunk_taken(const spa_paged_attend_args* a) {
-    return a->kv.Hkv > 0 && paged_chunk_taken(a->kv.format, a->seq_start, a->idx, a->T, a->Hq, a->kv.Hkv, a->kv.B,
+    return a->kv.Hkv > 0 && paged_chunk_taken(a->seq_start, a->idx, a->T, a->Hq, a->kv.Hkv, a->kv.B,
                                               a->sm_scale);
 }
 

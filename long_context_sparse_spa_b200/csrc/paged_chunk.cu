@@ -1,8 +1,8 @@
-// Exact softmax attention of many new tokens per sequence over a 4-bit paged KV cache (a prefill chunk
+// Exact softmax attention of many new tokens per sequence over a paged KV cache, 4-bit or bf16 (a prefill chunk
 // against its cached prefix, drafted tokens of a large batch) on tcgen05 tensor cores.
 //
 // A unit is up to 256 (query token, head) rows that share one (sequence, kv head): two tiles of 128 rows.
-// Per 128 cached tokens and row tile:
+// Per 128 cached tokens and row tile, 4-bit rows:
 //   S = Q K^T        fp16 x fp16, fp32 in TMEM; K = scale * (code - 8) has at most 8 + 3 significant bits,
 //                    so it is exact in fp16 once a power of two per 64 tokens (per token where some queries
 //                    do not see all of them) brings the scales into range;
@@ -11,11 +11,13 @@
 //   O += P V         P as the TMEM operand, V exact in fp16 like K; fp32 in TMEM
 // with the online softmax's reference per row following (logit + V's power of two); it moves, and O is
 // rescaled through TMEM, only when it is exceeded by 2^6.  l is summed in fp32.
+// bf16 rows: S = Q K^T and O += P V in bf16, fp32 in TMEM, with P = hi + lo (about 16 bits): two products per
+// weight, both parts over their logits in TMEM.
 //
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row); 8-15 unpack the cache (8-11 keys, 12-15
 // values; a thread has half of a token's codes); 16 and 17 issue the MMAs of row tile 0 and 1; 18 copies raw
-// rows, up to three steps of 64 tokens ahead, one bulk copy per run of tokens that lie together on a page.  The
-// unpacked K and V tiles are double-buffered.  A row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
+// rows, up to three steps of 64 tokens ahead, one bulk copy per run of tokens that lie together on a page.  (bf16:
+// 8-15 copy the rows to their swizzled places themselves, 16 bytes a copy, three steps in flight.)  The K and V tiles are double-buffered.  A row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
 // order, so an observed S(t) also means that P(t-1) V is complete and O may be read and rescaled; while one row
 // tile is in its softmax the tensor cores work for the other.
 //
@@ -27,7 +29,8 @@
 // products 1500, exponentials 2050 at 16 a clock for both row tiles together, TMEM reads and barriers); without the
 // exponentials the same kernel takes 426 us, without the unpacking 577, with one product in eight 518.  Steps that
 // counted: four to eight unpacking warps 1128 -> 892, the weights' product not waiting for the next keys -> 805,
-// loops over 32 columns kept rolled (the roles share the instruction cache) -> 666.
+// loops over 32 columns kept rolled (the roles share the instruction cache) -> 666.  The same from bf16 pages
+// (708 GFLOP with the weights' two parts, 439 us at that rate): 711 us, where the mma.sync kernel takes 3282.
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -49,7 +52,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kBase = 9.f, kSlack = 6.f;
 constexpr uint32_t kSpin = 1u << 22;
 
-template <int D>
+template <int D, bool INT4>
 struct ChunkShared {
     static constexpr int kSlabs = D / 64;
     static constexpr int kTile = kSlabs * kSlab;       // 128 rows of D fp16
@@ -57,7 +60,7 @@ struct ChunkShared {
     uint8_t k[2][kTile];
     uint8_t v[2][kTile];
     static constexpr int ROWB = D + 16;
-    uint8_t raw[3][kHalf * ROWB];
+    uint8_t raw[3][INT4 ? kHalf * ROWB : 16];
     uint64_t raw_full[3], raw_empty[3];
     uint32_t raw_valid[3][2];                          // tokens of the step that exist
     uint64_t s_full[2], p_full[2][2], pv_half[2];      // by row tile (and half of the tokens)
@@ -65,7 +68,11 @@ struct ChunkShared {
     int ek[4][2], ev[4][2];                            // the powers of two of tile t (slot t % 4), by half
     alignas(16) int8_t ek1[4][kKeys];                  // ... of a tile that not all queries see whole: by token
     alignas(16) int8_t ev1[4][kKeys];
-    uint32_t poison[4][4][4];                          // tile t: tokens whose values of group g are not finite
+    uint32_t poison[4][4][4];                          // 4-bit, tile t: tokens whose values of group g are not finite
+    // bf16, tile t (one that not all queries see whole): by token, a bit for each channel whose value is not finite,
+    // and whether a warp found one in a half
+    alignas(16) uint8_t bad[INT4 ? 1 : 4][kKeys][D / 8];
+    uint32_t any_bad[4][2][kUnpack / 2];
     uint32_t tmem_base;
     int fail;                                          // a bounded wait gave up
     int last;
@@ -78,6 +85,10 @@ __device__ __forceinline__ float bf_hi(uint32_t x) { return __uint_as_float(x & 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(uint32_t(127 + e) << 23); }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
@@ -177,8 +188,9 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// floats of one share of a split unit: O [D / 4][256][4], then m, l and the poisoned groups of each row
-__host__ __device__ constexpr int chunk_rec_floats(int d) { return 256 * (d + 3); }
+// floats of one share of a split unit: O [D / 4][256][4], then m, l and four words of poisoned groups (4-bit: the
+// first) or channels of each row
+__host__ __device__ constexpr int chunk_rec_floats(int d) { return 256 * (d + 6); }
 
 struct SeqG { int n, len, row0; };
 __device__ __forceinline__ SeqG seq_geo(const PagedAttendParams& p, int b, bool* bad) {
@@ -199,11 +211,12 @@ __device__ __forceinline__ long long head_weight(const SeqG& s, int TQ) {
     return w;
 }
 
-template <int D>
+template <int D, bool INT4>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
-    using SH = ChunkShared<D>;
+    using SH = ChunkShared<D, INT4>;
     static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && SH::ROWB % 16 == 0 && offsetof(SH, ek1) % 16 == 0 &&
                   sizeof(SH) % 8 == 0, "alignment of shared accesses");
+    constexpr int NW = INT4 ? 1 : D / 32;              // words of poisoned groups or channels
     constexpr int WORDS = D / 8;                       // 16-byte pieces of an operand row, code words of a row
     extern __shared__ __align__(1024) uint8_t dyn[];
     SH& sh = *reinterpret_cast<SH*>(dyn);
@@ -358,7 +371,97 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         tiles_done += uint32_t(nt);
         if (ntile == 2) tiles1_done += uint32_t(nt);
 
-        if (warp >= 8 && warp < 8 + kUnpack) {
+        if (!INT4 && warp >= 8 && warp < 8 + kUnpack) {
+            // ================================================================ bf16 rows
+            // Warps 8-11 copy the keys and 12-15 the values of 64 tokens at a time to their swizzled places, 16 bytes a
+            // copy, three steps in flight.  A lane looks up the page of one run of tokens, a step ahead.
+            constexpr int CH = D / 8, PER = kHalf * CH / 128;  // pieces of a row, and of a thread's step
+            const bool isv = warp >= 12;
+            const int ut = (tid - 256) & 127, c = ut % CH;     // this thread's piece, of tokens ut / CH + k (128 / CH)
+            const int rsh = min(6, p.kv.page_shift), R = 1 << rsh, runs = kHalf >> rsh;
+            const int32_t* const pt = p.kv.page_table + (long long)(g0 + grp) * p.kv.max_pages;
+            const int steps = 2 * nt;
+            auto page_of = [&](int h) -> int {                 // (lim <= len: inside the table)
+                const int n = a * kKeys + h * kHalf + lane * R;
+                return h < steps && lane < runs && n < lim ? __ldg(pt + (n >> p.kv.page_shift)) : -1;
+            };
+            auto place = [&](int h, int k) -> uint8_t* {       // of piece k of step h
+                const int r = (h & 1) * kHalf + ut / CH + k * (128 / CH);
+                uint8_t* const tile = isv ? sh.v[(base + uint32_t(h >> 1)) & 1] : sh.k[(base + uint32_t(h >> 1)) & 1];
+                return tile + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            };
+            auto finish = [&](int h) {                         // step h has landed
+                const uint32_t T = base + uint32_t(h >> 1);
+                if (isv && (a + (h >> 1) + 1) * kKeys > lim0) {
+                    // Tokens that some of the unit's queries do not see: values that are not finite are taken as 0 (0 * NaN
+                    // would reach every query) and noted for those that do see them.
+                    bool found = false;
+#pragma unroll
+                    for (int k = 0; k < PER; ++k) {
+                        uint4* const at = reinterpret_cast<uint4*>(place(h, k));
+                        const uint4 w = *at;
+                        uint32_t u4[4] = {w.x, w.y, w.z, w.w}, bits = 0;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if ((u4[i] & 0x7f80u) == 0x7f80u) { bits |= 1u << (2 * i); u4[i] &= 0xffff0000u; }
+                            if ((u4[i] & 0x7f800000u) == 0x7f800000u) { bits |= 2u << (2 * i); u4[i] &= 0xffffu; }
+                        }
+                        sh.bad[T & 3][(h & 1) * kHalf + ut / CH + k * (128 / CH)][c] = uint8_t(bits);
+                        if (bits) *at = make_uint4(u4[0], u4[1], u4[2], u4[3]);
+                        found |= bits != 0;
+                    }
+                    found = __any_sync(0xffffffffu, found);
+                    if (lane == 0) sh.any_bad[T & 3][h & 1][warp - 12] = found;
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) arrive(isv ? &sh.v_full[T & 1] : &sh.k_full[T & 1]);
+            };
+            int pid = page_of(0), h = 0;
+            for (; h < steps; ++h) {
+                const uint32_t T = base + uint32_t(h >> 1);
+                const int n = a * kKeys + h * kHalf + lane * R;
+                int rows = lane < runs ? min(max(lim - n, 0), R) : 0;
+                long long off = rows > 0 ? paged_row(p.kv, pid, g, n) : -1;
+                if (rows > 0 && off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+                if (off < 0) off = rows = 0;
+                pid = page_of(h + 1);
+                if ((h & 1) == 0 && T >= 2 &&              // the tile two back has been read
+                    !__all_sync(0xffffffffu, wait(isv ? &sh.v_empty[T & 1] : &sh.k_empty[T & 1], ((T >> 1) - 1) & 1)))
+                    break;
+                if (warp == 8) {                           // tokens of the step that exist
+                    const unsigned long long m =
+                        rows > 0 ? (rows >= 64 ? ~0ull : (1ull << rows) - 1) << (lane * R & 63) : 0ull;
+                    const uint32_t m0 = __reduce_or_sync(0xffffffffu, uint32_t(m));
+                    const uint32_t m1 = __reduce_or_sync(0xffffffffu, uint32_t(m >> 32));
+                    if (lane == 0) {
+                        sh.valid[T & 3][2 * (h & 1)] = m0;
+                        sh.valid[T & 3][2 * (h & 1) + 1] = m1;
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < PER; ++k) {
+                    const int tok = ut / CH + k * (128 / CH), run = tok >> rsh, i = tok & (R - 1);
+                    const long long o = __shfl_sync(0xffffffffu, off, run);
+                    const bool there = i < __shfl_sync(0xffffffffu, rows, run);
+                    const uint8_t* const src = p.kv.data + (there ? o + i * (4 * D) + (isv ? 2 * D : 0) + c * 16 : 0);
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(place(h, k))), "l"(src),
+                                 "r"(there ? 16 : 0)       // (zeros where there is no token)
+                                 : "memory");
+                }
+                asm volatile("cp.async.commit_group;\n" ::: "memory");
+                if (h >= 2) {
+                    asm volatile("cp.async.wait_group 2;\n" ::: "memory");
+                    finish(h - 2);
+                }
+            }
+            asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+            if (h == steps) {
+                finish(h - 2);                             // (steps is even)
+                finish(h - 1);
+            }
+            __syncwarp();
+        } else if (INT4 && warp >= 8 && warp < 8 + kUnpack) {
             // ================================================================ unpacking
             // Keys and values have their own warps, which meet only at the raw rows, three steps deep.
             const bool isv = warp >= 12;
@@ -480,8 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             // ================================================================ MMA issue
             // A warp per row tile, so that neither waits for the other's weights (one warp for both: 696 us, see the file's
             // table).  The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.
-            constexpr uint32_t kIdS = idesc_f16(128, kKeys, false);
-            constexpr uint32_t kIdO = idesc_f16(128, D, true);
+            constexpr uint32_t kIdS = INT4 ? idesc_f16(128, kKeys, false) : idesc_bf16(128, kKeys, false);
+            constexpr uint32_t kIdO = INT4 ? idesc_f16(128, D, true) : idesc_bf16(128, D, true);
             const uint64_t dq0 = sw128_desc(smem_u32(sh.q[0]), 16, 1024);
             const uint64_t dk0 = sw128_desc(smem_u32(sh.k[0]), 16, 1024);
             const uint64_t dv0 = sw128_desc(smem_u32(sh.v[0]), kSlab, 1024);
@@ -511,8 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 const uint32_t acc0 = !first || h > 0 ? 1u : 0u;
                 if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < kHalf / 16; ++kk)
-                        umma_ts(dst, src + kk * 8, dv + uint64_t((kk * 2048) >> 4), kIdO, kk > 0 ? 1u : acc0);
+                    for (int kk = 0; kk < kHalf / 16; ++kk) {
+                        const uint64_t dk16 = dv + uint64_t((kk * 2048) >> 4);
+                        if constexpr (INT4) {
+                            umma_ts(dst, src + kk * 8, dk16, kIdO, kk > 0 ? 1u : acc0);
+                        } else {                       // of 32 tokens the high parts, then the low parts
+                            umma_ts(dst, src + (kk >> 1) * 32 + (kk & 1) * 8, dk16, kIdO, kk > 0 ? 1u : acc0);
+                            umma_ts(dst, src + (kk >> 1) * 32 + (kk & 1) * 8 + 16, dk16, kIdO, 1u);
+                        }
+                    }
                     if (h == 0) umma_commit(&sh.pv_half[i]);
                 }
                 __syncwarp();
@@ -557,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             if (part) commit(&sh.o_done);
             if (part && !live) wait(&sh.o_done, segs & 1);   // what was issued before a wait gave up
             __syncwarp();
-        } else if (warp == 8 + kUnpack + 2) {
+        } else if (INT4 && warp == 8 + kUnpack + 2) {
             // ================================================================ raw rows
             constexpr int ROWB = SH::ROWB;
             const int rsh = min(6, p.kv.page_shift), R = 1 << rsh, runs = kHalf >> rsh;   // runs of R tokens per step
@@ -618,7 +728,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             const uint32_t t_o = t_s + 256;
             const int lim_r = have ? lim0 + row / G : lim;
             float hrow;
-            if (rt < ntile) {
+            if (!INT4 && rt < ntile) {
+                const uint16_t* src = p.q + (have ? (row0 + row / G) * p.q_tok + (g * G + row % G) * p.q_head : 0);
+                hrow = sl2;
+#pragma unroll
+                for (int c = 0; c < WORDS; ++c)
+                    *reinterpret_cast<uint4*>(sh.q[rt] + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+            }
+            if (INT4 && rt < ntile) {
                 // this row of Q: its largest channel to [2^13, 2^14), pieces and order as the keys'
                 const uint16_t* src = p.q + (have ? (row0 + row / G) * p.q_tok + (g * G + row % G) * p.q_head : 0);
                 uint4 w[WORDS];
@@ -665,19 +784,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 
             auto n0_of = [&](int t) { return (a + t) * kKeys; };
             float m = -INFINITY, l = 0.f;
-            uint32_t nan = 0;                              // groups of V that are not finite in a token it sees
+            uint32_t nan[NW] = {};                         // groups (bf16: channels) of V that are not finite in a token it sees
             // values of tile t are unpacked once P(t) V is complete, which S(t + 1) shows
             auto poisoned = [&](int t) {
                 if (n0_of(t) + kKeys <= lim0) return;
                 const int seen = lim_r - n0_of(t);
+                const int slot = (base + uint32_t(t)) & 3;
+                if constexpr (INT4) {
 #pragma unroll
-                for (int gr = 0; gr < 4; ++gr)
+                    for (int gr = 0; gr < 4; ++gr)
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const int c = seen - 32 * w;
-                        const uint32_t vis = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
-                        if (sh.poison[(base + uint32_t(t)) & 3][gr][w] & vis) nan |= 1u << gr;
-                    }
+                        for (int w = 0; w < 4; ++w) {
+                            const int c = seen - 32 * w;
+                            const uint32_t vis = c >= 32 ? 0xffffffffu : c <= 0 ? 0u : (1u << c) - 1u;
+                            if (sh.poison[slot][gr][w] & vis) nan[0] |= 1u << gr;
+                        }
+                } else {
+                    uint32_t any = 0;
+                    for (int i = 0; i < kUnpack; ++i) any |= sh.any_bad[slot][i >> 2][i & 3];
+                    if (!any) return;
+#pragma unroll 1
+                    for (int i = 0; i < seen && i < kKeys; ++i)
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) nan[w] |= *reinterpret_cast<const uint32_t*>(&sh.bad[slot][i][4 * w]);
+                }
             };
             bool ok = rt < ntile;
             for (int t = 0; ok && t < nt; ++t) {
@@ -690,8 +820,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 const uint32_t vm[4] = {vd.x, vd.y, vd.z, vd.w};
                 const bool edge = n0 + kKeys > lim0, gaps = (vm[0] & vm[1] & vm[2] & vm[3]) != 0xffffffffu;
                 const int seen = lim_r - n0;               // columns below this one are seen
-                float cs[2] = {1.f, 1.f}, ev[2] = {0.f, 0.f};
-                if (!edge) {
+                float cs[2] = {hrow, hrow}, ev[2] = {0.f, 0.f};
+                if (INT4 && !edge) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         cs[h] = hrow * pow2i(sh.ek[T & 3][h]);
@@ -702,6 +832,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 auto masked = [&](int q4, float (&v)[32]) {
 #pragma unroll
                     for (int i4 = 0; i4 < 8; ++i4) {
+                        if constexpr (!INT4) {
+#pragma unroll
+                            for (int i = 4 * i4; i < 4 * i4 + 4; ++i)
+                                v[i] = ((vm[q4] >> i) & 1u) && q4 * 32 + i < seen ? v[i] * hrow : -INFINITY;
+                            continue;
+                        }
                         const char4 e = reinterpret_cast<const char4*>(sh.ek1[T & 3])[q4 * 8 + i4];
                         const char4 f = reinterpret_cast<const char4*>(sh.ev1[T & 3])[q4 * 8 + i4];
                         const int ee[4] = {e.x, e.y, e.z, e.w}, ff[4] = {f.x, f.y, f.z, f.w};
@@ -759,7 +895,39 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                     }
                     return top;
                 };
-                if (edge || gaps) {
+                if constexpr (!INT4) {
+                    // The maximum first, then the weights as two bf16 numbers of 32 tokens at a time, over their logits.
+                    if (edge && t > 0) poisoned(t - 1);
+                    const float top = top_of(0, 4);
+                    if (__any_sync(0xffffffffu, top > m + kSlack)) follow(top, 0);
+                    const float ref = m == -INFINITY ? 0.f : kBase - m;
+                    float sum[2] = {0.f, 0.f};
+#pragma unroll 1
+                    for (int q4 = 0; q4 < 4; ++q4) {
+                        float v[32];
+                        tmem_ld32(t_s + q4 * 32, v);
+                        float c = hrow;
+                        if (edge || gaps) {
+                            masked(q4, v);
+                            c = 1.f;
+                        }
+                        uint32_t hi[16], lo[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float x0 = v[2 * i], x1 = v[2 * i + 1];
+                            ffma2(x0, x1, c, ref);
+                            x0 = ex2_approx(x0);
+                            x1 = ex2_approx(x1);
+                            hi[i] = pack_bf16(x0, x1);
+                            lo[i] = pack_bf16(x0 - bf_lo(hi[i]), x1 - bf_hi(hi[i]));
+                            fadd2(sum[0], sum[1], x0, x1);
+                        }
+                        tmem_st16(t_s + q4 * 32, hi);
+                        tmem_st16(t_s + q4 * 32 + 16, lo);
+                        if (q4 & 1) done(q4 >> 1);
+                    }
+                    l += sum[0] + sum[1];
+                } else if (edge || gaps) {
                     if (t > 0) poisoned(t - 1);
                     const float top = top_of(0, 4);
                     if (__any_sync(0xffffffffu, top > m + kSlack)) follow(top, 0);
@@ -842,13 +1010,34 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             // 32 columns of this row: column 64 hh + 8 r + q of O is channel 64 hh + r + 32 (q % 2) + 8 (q / 2), held
             // times 2^-21, or 2^-17 where its code is odd (q / 2 odd)
             auto put = [&](int n, const float (&o)[32], float L) {
+                if constexpr (!INT4) {                 // column n of O is channel n
+                    const float il = L == 0.f ? 0.f : 1.f / L;
+                    const size_t at = (size_t(row0 + row / G) * p.Hq + g * G + row % G) * D + n;
+                    uint32_t nb = 0;
+#pragma unroll
+                    for (int w = 0; w < NW; ++w)
+                        if (n == 32 * w) nb = nan[w];
+#pragma unroll
+                    for (int q = 0; q < 32; q += 4) {
+                        auto val = [&](int k) { return (nb >> (q + k)) & 1u ? __uint_as_float(0x7fc00000u) : o[q + k] * il; };
+                        const float4 y = make_float4(val(0), val(1), val(2), val(3));
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
+                        *reinterpret_cast<uint2*>(p.out + at + q) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        if (p.out_f32) *reinterpret_cast<float4*>(p.out_f32 + at + q) = y;
+                    }
+                    if (p.lse && n == 0)
+                        p.lse[size_t(row0 + row / G) * p.Hq + g * G + row % G] =
+                            L == 0.f ? -INFINITY : (m - kBase + log2f(L)) * kLn2;
+                    return;
+                }
                 const float il = (L == 0.f ? 0.f : 1.f / L) * 2097152.f;
                 const int hh = n >> 6, r8 = (n & 63) >> 3;             // four r from r8 on
                 const size_t at = (size_t(row0 + row / G) * p.Hq + g * G + row % G) * D;
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const int ch = 64 * hh + r8 + 32 * (q & 1) + 8 * (q >> 1);
-                    const bool bad = (nan >> (ch / (D / 4))) & 1u;
+                    const bool bad = (nan[0] >> (ch / (D / 4))) & 1u;
                     const float f = bad ? __uint_as_float(0x7fc00000u) : (q >> 1) & 1 ? il * 0.0625f : il;
                     const float4 y = make_float4(o[q] * f, o[8 + q] * f, o[16 + q] * f, o[24 + q] * f);
                     const __nv_bfloat162 lo = __floats2bfloat162_rn(y.x, y.y), hi = __floats2bfloat162_rn(y.z, y.w);
@@ -878,7 +1067,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 if (!whole) {
                     part[256 * D + row] = m;
                     part[256 * D + 256 + row] = l;
-                    part[256 * D + 512 + row] = __uint_as_float(nan);
+#pragma unroll
+                    for (int w = 0; w < NW; ++w) part[256 * D + (2 + w) * 256 + row] = __uint_as_float(nan[w]);
                 }
             }
             tc_fence_before();
@@ -904,7 +1094,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         L += (mk == -INFINITY ? 0.f : ex2_approx(mk - M)) * __ldcg(slot(k) + 256 * D + 256 + row);
                     }
                     m = M;
-                    for (int k = 0; k < n; ++k) nan |= __float_as_uint(__ldcg(slot(k) + 256 * D + 512 + row));
+                    for (int k = 0; k < n; ++k)
+#pragma unroll
+                        for (int w = 0; w < NW; ++w) nan[w] |= __float_as_uint(__ldcg(slot(k) + 256 * D + (2 + w) * 256 + row));
 #pragma unroll 1
                     for (int nn = 0; nn < D; nn += 32) {
                         float o[32];
@@ -960,16 +1152,16 @@ spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st) {
     if (step < 1) return SPA_ERR_UNSUPPORTED_SHAPE;
     for (int g0 = 0; g0 < p.kv.B; g0 += int(step)) {
         const int groups = p.kv.B - g0 < step ? p.kv.B - g0 : int(step);
-#define SPA_PC(DD)                                                                                              \
-    if (p.kv.d == DD) {                                                                                         \
-        constexpr size_t kMost = sizeof(ChunkShared<DD>) + size_t(kChunkUnits + 1) * 4;                          \
+#define SPA_PC(DD, I4)                                                                                          \
+    if (p.kv.d == DD && (p.kv.int4 != 0) == I4) {                                                               \
+        constexpr size_t kMost = sizeof(ChunkShared<DD, I4>) + size_t(kChunkUnits + 1) * 4;                      \
         static_assert(kMost <= 227 * 1024, "paged chunk: shared memory over the per-CTA limit");                 \
-        SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_chunk_kernel<DD>),                        \
+        SPA_CUDA_TRY(set_func_attr(reinterpret_cast<const void*>(paged_chunk_kernel<DD, I4>),                    \
                                    cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)));                   \
-        SPA_CUDA_TRY(launch_pdl(paged_chunk_kernel<DD>, dim3(sms), dim3(kThreads),                               \
-                                sizeof(ChunkShared<DD>) + size_t(groups + 1) * 4, st, p, g0, groups, TQ));        \
+        SPA_CUDA_TRY(launch_pdl(paged_chunk_kernel<DD, I4>, dim3(sms), dim3(kThreads),                           \
+                                sizeof(ChunkShared<DD, I4>) + size_t(groups + 1) * 4, st, p, g0, groups, TQ));    \
     }
-        SPA_PC(64) SPA_PC(128)
+        SPA_PC(64, false) SPA_PC(64, true) SPA_PC(128, false) SPA_PC(128, true)
 #undef SPA_PC
     }
     return SPA_OK;

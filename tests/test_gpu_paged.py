@@ -434,6 +434,92 @@ def test_chunk_masks_what_is_not_finite_and_bad_pages():
             check_attention(c, _bf(q)[t], o, lse[t], [sees], 0.09, 0, f"row {t}")
 
 
+def test_bf16_units_of_one_and_two_row_tiles_in_turn():
+    rng = np.random.default_rng(53)
+    new = [int(x) for x in rng.choice([3, 20, 40, 64, 33, 50], 180)]
+    lens = [int(n + x) for n, x in zip(new, rng.integers(0, 700, 180))]
+    c = Cache(lens, 2, 64, 32, BF16, seed=53)
+    start = np.concatenate(([0], np.cumsum(new)))
+    q = torch.randn(int(start[-1]), 8, 64, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.15, seq_start=_i32(start), **c.kw)
+    out, lse, qv = _bf(plan.out), _np(plan.lse).astype(np.float64), _bf(q)
+    for b in range(0, 180, 7):
+        for i in (0, new[b] // 2, new[b] - 1):
+            t = start[b] + i
+            check_attention(c, qv[t], out[t], lse[t], [np.arange(lens[b]) <= lens[b] - new[b] + i] * 2, 0.15, b,
+                            f"sequence {b}, query {i}")
+    first = plan.out.clone()
+    for _ in range(20):
+        plan.run()
+        assert torch.equal(first, plan.out)
+    assert spa.read_device_status(plan.ws) == 0
+
+
+@pytest.mark.parametrize("qs,ks,vs", [(1, 1, 1e-30), (1, 1, 1e30), (1e-20, 1e20, 1), (1e15, 1e-15, 1e-6), (40, 1, 1)])
+def test_bf16_chunk_scales_far_from_one(qs, ks, vs):
+    c = Cache([400], 1, 128, 16, BF16, seed=54, kscale=ks, vscale=vs)
+    q = (qs * torch.randn(60, 4, 128, device="cuda")).to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32([0, 60]), **c.kw)
+    for t in (0, 33, 59):
+        check_attention(c, _bf(q)[t], _bf(plan.out)[t], _np(plan.lse)[t].astype(np.float64), [np.arange(400) <= 340 + t],
+                        0.09, 0, f"row {t}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("L", [300, 20_000])     # the longer one is split, and its shares merged
+def test_bf16_chunk_masks_what_is_not_finite_and_bad_pages(d, L):
+    c = Cache([L], 1, d, 16, BF16, seed=55)
+    pool = c.pool
+    hit = np.zeros(d, bool)
+    hit[[0, 5, d - 1]] = True
+    # token L - 40: its value in three channels; token L - 10: its key; tokens 64-79: no page
+    n1, n2 = L - 40, L - 10
+    for ch, x in zip(np.flatnonzero(hit), (np.nan, np.inf, -np.inf)):
+        pool[int(c.table[0, n1 // 16]), 0, n1 % 16, 1, int(ch)] = float(x)
+    pool[int(c.table[0, n2 // 16]), 0, n2 % 16, 0, 7] = float("nan")
+    c.kw["page_table"][0, 4] = 1 << 30
+    q = torch.randn(60, 4, d, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32([0, 60]), **c.kw)
+    assert spa.read_device_status(plan.ws) == INVALID
+    out, lse, n = _bf(plan.out), _np(plan.lse).astype(np.float64), np.arange(L)
+    for t in (0, 10, 19, 20, 40, 49, 50, 59):
+        sees = (n <= L - 60 + t) & ((n < 64) | (n >= 80))
+        if t >= 50:
+            assert np.isnan(out[t]).all() and np.isnan(lse[t]).all()
+            continue
+        o = out[t].copy()
+        if t >= 20:
+            assert not np.isfinite(o[:, hit]).any() and np.isfinite(o[:, ~hit]).all()
+            o[:, hit] = 0
+            keep = c.V[0].copy()
+            c.V[0][:, :, hit] = 0
+            check_attention(c, _bf(q)[t], o, lse[t], [sees], 0.09, 0, f"row {t}")
+            c.V[0] = keep
+        else:
+            check_attention(c, _bf(q)[t], o, lse[t], [sees], 0.09, 0, f"row {t}")
+
+
+def test_bf16_chunks_on_two_streams():
+    cs = [Cache([700, 90, 300], 2, d, 16, BF16, seed=s, extra=2) for s, d in ((56, 128), (57, 64))]
+    start = [0, 60, 61, 161]
+    qs = [torch.randn(161, 8, c.d, device="cuda").to(torch.bfloat16) for c in cs]
+    plans = [spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32(start), run=False, **c.kw) for c, q in zip(cs, qs)]
+    streams = [torch.cuda.Stream() for _ in plans]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s in zip(plans, streams):
+            p.run(s)
+    torch.cuda.synchronize()
+    for c, q, p in zip(cs, qs, plans):
+        assert spa.read_device_status(p.ws) == 0
+        for b, L in enumerate([700, 90, 300]):
+            n = start[b + 1] - start[b]
+            for i in (0, n - 1):
+                t = start[b] + i
+                check_attention(c, _bf(q)[t], _bf(p.out)[t], _np(p.lse)[t].astype(np.float64),
+                                [np.arange(L) <= L - n + i] * 2, 0.1, b, f"row {t}")
+
+
 def test_queries_before_the_first_token_see_nothing():
     c = Cache([3], 1, 128, 16, INT4, seed=1)
     q = torch.randn(5, 4, 128, device="cuda").to(torch.bfloat16)
