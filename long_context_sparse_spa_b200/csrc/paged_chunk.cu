@@ -17,9 +17,10 @@
 // Warps: 0-3 and 4-7 softmax of row tile 0 and 1 (a thread is a row); 8-15 unpack the cache (8-11 keys, 12-15
 // values; a thread has half of a token's codes); 16 and 17 issue the MMAs of row tile 0 and 1; 18 copies raw
 // rows, up to three steps of 64 tokens ahead, one bulk copy per run of tokens that lie together on a page.  (bf16:
-// 8-15 copy the rows to their swizzled places themselves, 16 bytes a copy, three steps in flight.)  The K and V tiles are double-buffered.  A row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue
-// order, so an observed S(t) also means that P(t-1) V is complete and O may be read and rescaled; while one row
-// tile is in its softmax the tensor cores work for the other.
+// 8-15 copy the rows to their swizzled places themselves, 16 bytes a copy, three steps in flight.)  The K and V tiles
+// are double-buffered.  A row tile's chain S(t) -> P(t) -> O += P V, S(t+1) is in issue order, so an observed S(t)
+// also means that P(t-1) V is complete and O may be read and rescaled; while one row tile is in its softmax the
+// tensor cores work for the other.
 //
 // Units are split evenly over the SMs by 128-token tiles as in paged_attend.cu; the last CTA of a split
 // unit merges its shares in the order of the CTAs.
@@ -71,8 +72,8 @@ struct ChunkShared {
     uint32_t poison[4][4][4];                          // 4-bit, tile t: tokens whose values of group g are not finite
     // bf16, tile t (one that not all queries see whole): by token, a bit for each channel whose value is not finite,
     // and whether a warp found one in a half
-    alignas(16) uint8_t bad[INT4 ? 1 : 4][kKeys][D / 8];
-    uint32_t any_bad[4][2][kUnpack / 2];
+    alignas(16) uint8_t bad[INT4 ? 1 : 4][INT4 ? 1 : kKeys][D / 8];
+    uint32_t any_bad[INT4 ? 1 : 4][2][kUnpack / 2];
     uint32_t tmem_base;
     int fail;                                          // a bounded wait gave up
     int last;
@@ -371,212 +372,215 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         tiles_done += uint32_t(nt);
         if (ntile == 2) tiles1_done += uint32_t(nt);
 
-        if (!INT4 && warp >= 8 && warp < 8 + kUnpack) {
-            // ================================================================ bf16 rows
-            // Warps 8-11 copy the keys and 12-15 the values of 64 tokens at a time to their swizzled places, 16 bytes a
-            // copy, three steps in flight.  A lane looks up the page of one run of tokens, a step ahead.
-            constexpr int CH = D / 8, PER = kHalf * CH / 128;  // pieces of a row, and of a thread's step
-            const bool isv = warp >= 12;
-            const int ut = (tid - 256) & 127, c = ut % CH;     // this thread's piece, of tokens ut / CH + k (128 / CH)
-            const int rsh = min(6, p.kv.page_shift), R = 1 << rsh, runs = kHalf >> rsh;
-            const int32_t* const pt = p.kv.page_table + (long long)(g0 + grp) * p.kv.max_pages;
-            const int steps = 2 * nt;
-            auto page_of = [&](int h) -> int {                 // (lim <= len: inside the table)
-                const int n = a * kKeys + h * kHalf + lane * R;
-                return h < steps && lane < runs && n < lim ? __ldg(pt + (n >> p.kv.page_shift)) : -1;
-            };
-            auto place = [&](int h, int k) -> uint8_t* {       // of piece k of step h
-                const int r = (h & 1) * kHalf + ut / CH + k * (128 / CH);
-                uint8_t* const tile = isv ? sh.v[(base + uint32_t(h >> 1)) & 1] : sh.k[(base + uint32_t(h >> 1)) & 1];
-                return tile + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
-            };
-            auto finish = [&](int h) {                         // step h has landed
-                const uint32_t T = base + uint32_t(h >> 1);
-                if (isv && (a + (h >> 1) + 1) * kKeys > lim0) {
-                    // Tokens that some of the unit's queries do not see: values that are not finite are taken as 0 (0 * NaN
-                    // would reach every query) and noted for those that do see them.
-                    bool found = false;
+        if (warp >= 8 && warp < 8 + kUnpack) {
+            // (The two formats part inside the role: as two branches of this chain the 4-bit kernel came out 4 % slower.)
+            if constexpr (!INT4) {
+                // ================================================================ bf16 rows
+                // Warps 8-11 copy the keys and 12-15 the values of 64 tokens at a time to their swizzled places, 16 bytes a
+                // copy, three steps in flight.  A lane looks up the page of one run of tokens, a step ahead.
+                constexpr int CH = D / 8, PER = kHalf * CH / 128;  // pieces of a row, and of a thread's step
+                const bool isv = warp >= 12;
+                const int ut = (tid - 256) & 127, c = ut % CH;     // this thread's piece, of tokens ut / CH + k (128 / CH)
+                const int rsh = min(6, p.kv.page_shift), R = 1 << rsh, runs = kHalf >> rsh;
+                const int32_t* const pt = p.kv.page_table + (long long)(g0 + grp) * p.kv.max_pages;
+                const int steps = 2 * nt;
+                auto page_of = [&](int h) -> int {                 // (lim <= len: inside the table)
+                    const int n = a * kKeys + h * kHalf + lane * R;
+                    return h < steps && lane < runs && n < lim ? __ldg(pt + (n >> p.kv.page_shift)) : -1;
+                };
+                auto place = [&](int h, int k) -> uint8_t* {       // of piece k of step h
+                    const int r = (h & 1) * kHalf + ut / CH + k * (128 / CH);
+                    uint8_t* const tile = isv ? sh.v[(base + uint32_t(h >> 1)) & 1] : sh.k[(base + uint32_t(h >> 1)) & 1];
+                    return tile + (c >> 3) * kSlab + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+                };
+                auto finish = [&](int h) {                         // step h has landed
+                    const uint32_t T = base + uint32_t(h >> 1);
+                    if (isv && (a + (h >> 1) + 1) * kKeys > lim0) {
+                        // Tokens that some of the unit's queries do not see: values that are not finite are taken as 0 (0 * NaN
+                        // would reach every query) and noted for those that do see them.
+                        bool found = false;
+#pragma unroll
+                        for (int k = 0; k < PER; ++k) {
+                            uint4* const at = reinterpret_cast<uint4*>(place(h, k));
+                            const uint4 w = *at;
+                            uint32_t u4[4] = {w.x, w.y, w.z, w.w}, bits = 0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                if ((u4[i] & 0x7f80u) == 0x7f80u) { bits |= 1u << (2 * i); u4[i] &= 0xffff0000u; }
+                                if ((u4[i] & 0x7f800000u) == 0x7f800000u) { bits |= 2u << (2 * i); u4[i] &= 0xffffu; }
+                            }
+                            sh.bad[T & 3][(h & 1) * kHalf + ut / CH + k * (128 / CH)][c] = uint8_t(bits);
+                            if (bits) *at = make_uint4(u4[0], u4[1], u4[2], u4[3]);
+                            found |= bits != 0;
+                        }
+                        found = __any_sync(0xffffffffu, found);
+                        if (lane == 0) sh.any_bad[T & 3][h & 1][warp - 12] = found;
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) arrive(isv ? &sh.v_full[T & 1] : &sh.k_full[T & 1]);
+                };
+                int pid = page_of(0), h = 0;
+                for (; h < steps; ++h) {
+                    const uint32_t T = base + uint32_t(h >> 1);
+                    const int n = a * kKeys + h * kHalf + lane * R;
+                    int rows = lane < runs ? min(max(lim - n, 0), R) : 0;
+                    long long off = rows > 0 ? paged_row(p.kv, pid, g, n) : -1;
+                    if (rows > 0 && off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
+                    if (off < 0) off = rows = 0;
+                    pid = page_of(h + 1);
+                    if ((h & 1) == 0 && T >= 2 &&              // the tile two back has been read
+                        !__all_sync(0xffffffffu, wait(isv ? &sh.v_empty[T & 1] : &sh.k_empty[T & 1], ((T >> 1) - 1) & 1)))
+                        break;
+                    if (warp == 8) {                           // tokens of the step that exist
+                        const unsigned long long m =
+                            rows > 0 ? (rows >= 64 ? ~0ull : (1ull << rows) - 1) << (lane * R & 63) : 0ull;
+                        const uint32_t m0 = __reduce_or_sync(0xffffffffu, uint32_t(m));
+                        const uint32_t m1 = __reduce_or_sync(0xffffffffu, uint32_t(m >> 32));
+                        if (lane == 0) {
+                            sh.valid[T & 3][2 * (h & 1)] = m0;
+                            sh.valid[T & 3][2 * (h & 1) + 1] = m1;
+                        }
+                    }
 #pragma unroll
                     for (int k = 0; k < PER; ++k) {
-                        uint4* const at = reinterpret_cast<uint4*>(place(h, k));
-                        const uint4 w = *at;
-                        uint32_t u4[4] = {w.x, w.y, w.z, w.w}, bits = 0;
+                        const int tok = ut / CH + k * (128 / CH), run = tok >> rsh, i = tok & (R - 1);
+                        const long long o = __shfl_sync(0xffffffffu, off, run);
+                        const bool there = i < __shfl_sync(0xffffffffu, rows, run);
+                        const uint8_t* const src = p.kv.data + (there ? o + i * (4 * D) + (isv ? 2 * D : 0) + c * 16 : 0);
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(place(h, k))), "l"(src),
+                                     "r"(there ? 16 : 0)       // (zeros where there is no token)
+                                     : "memory");
+                    }
+                    asm volatile("cp.async.commit_group;\n" ::: "memory");
+                    if (h >= 2) {
+                        asm volatile("cp.async.wait_group 2;\n" ::: "memory");
+                        finish(h - 2);
+                    }
+                }
+                asm volatile("cp.async.wait_group 0;\n" ::: "memory");
+                if (h == steps) {
+                    finish(h - 2);                             // (steps is even)
+                    finish(h - 1);
+                }
+                __syncwarp();
+            } else {
+                // ================================================================ unpacking
+                // Keys and values have their own warps, which meet only at the raw rows, three steps deep.
+                const bool isv = warp >= 12;
+                const int ut = (tid - 256) & 127, part = ut >> 6, tok = ut & 63;
+                constexpr int ROWB = SH::ROWB;
+                const int steps = 2 * nt;
+                for (int h = 0; h < steps; ++h) {
+                    const uint32_t T = base + uint32_t(h >> 1);        // tile over the kernel
+                    const int stage = T & 1, half = h & 1;
+                    const uint32_t S = base_raw + uint32_t(h), slot = S % 3;
+                    if (!__all_sync(0xffffffffu, wait(&sh.raw_full[slot], (S / 3) & 1))) break;
+                    const uint8_t* raw = sh.raw[slot];
+                    // powers of two: the largest scale (that is a number) of the 64 tokens to [2^15, 2^16)
+                    auto top = [](uint32_t w) -> uint32_t { return max(w & 0x7fffu, (w >> 16) & 0x7fffu); };   // of two bf16
+                    uint32_t kmx, vmx;
+                    {
+                        const uint4 s0 = *reinterpret_cast<const uint4*>(raw + lane * ROWB + D);
+                        const uint4 s1 = *reinterpret_cast<const uint4*>(raw + (lane + 32) * ROWB + D);
+                        kmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.x, s0.y), max_bf16x2(s1.x, s1.y)), 0u));
+                        vmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.z, s0.w), max_bf16x2(s1.z, s1.w)), 0u));
+                        if (isv) kmx = 0;                      // (only the first key warp needs both)
+                        else if (warp != 8) vmx = 0;
+                    }
+                    auto expo = [](uint32_t m) { return min(max(int(m >> 7) - 127, -70), 127) - 15; };
+                    const uint8_t* row = raw + tok * ROWB;
+                    const uint4 all = *reinterpret_cast<const uint4*>(row + D);
+                    // A tile that some queries do not see whole: every token has its own powers of two, so that what a
+                    // query does not see cannot push what it sees out of fp16's range.
+                    const bool edge = (a + (h >> 1) + 1) * kKeys > lim0;
+                    int ek, ev;
+                    if (edge) {
+                        ek = expo(top(max_bf16x2(max_bf16x2(all.x, all.y), 0u)));
+                        ev = expo(top(max_bf16x2(max_bf16x2(all.z, all.w), 0u)));
+                        if (!isv && part == 0) {
+                            sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
+                            sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
+                        }
+                    } else {
+                        ek = isv ? 0 : expo(__reduce_max_sync(0xffffffffu, kmx));
+                        ev = isv || warp == 8 ? expo(__reduce_max_sync(0xffffffffu, vmx)) : 0;
+                        if (!isv && ut == 0) {
+                            sh.ek[T & 3][half] = ek;
+                            sh.ev[T & 3][half] = ev;
+                        }
+                    }
+                    const uint2 sc = isv ? make_uint2(all.z, all.w) : make_uint2(all.x, all.y);
+                    const float mul = pow2i(isv ? -ev : -ek);
+                    float f[4] = {bf_lo(sc.x) * mul, bf_hi(sc.x) * mul, bf_lo(sc.y) * mul, bf_hi(sc.y) * mul};
+                    const int r = half * kHalf + tok;      // row of the operand tile
+                    if (isv && edge) {
+                        // Tokens that some of the unit's queries do not see: a group that is not finite is taken as 0
+                        // (0 * NaN would reach every query) and noted for those that do see it.
+                        const int n = (a + (h >> 1)) * kKeys + r;
+#pragma unroll
+                        for (int gr = 0; gr < 4; ++gr) {
+                            const bool nan = n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
+                            const uint32_t m = __ballot_sync(0xffffffffu, nan);
+                            if (lane == 0 && part == 0) sh.poison[T & 3][gr][r >> 5] = m;
+                            if (nan) f[gr] = 0.f;
+                        }
+                    }
+                    if (!isv && part == 0 && lane == 0) sh.valid[T & 3][r >> 5] = sh.raw_valid[slot][tok >> 5];
+                    if (half == 0 && T >= 2) {             // the tile two back has been read
+                        if (!__all_sync(0xffffffffu,
+                                        wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1)))
+                            break;
+                    }
+                    uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
+                    const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
+                    // scale pairs of a word's code pairs (0,4) (1,5) and (2,6) (3,7), for the words that differ in them
+                    Scale2 s2[4];
+                    if (D == 128) {
+                        if (isv) {                         // word 2 r + hh: groups 2 hh and 2 hh + 1
+                            s2[0] = s2[2] = scale2(f[0], f[1]);
+                            s2[1] = s2[3] = scale2(f[2], f[3]);
+                        } else {                           // word 4 t + g: group g
+#pragma unroll
+                            for (int gr = 0; gr < 4; ++gr) s2[gr] = scale2(f[gr], f[gr]);
+                        }
+                    } else {
+                        if (isv) {                         // word r: groups 0 and 2, then 1 and 3
+                            s2[0] = scale2(f[0], f[2]);
+                            s2[1] = scale2(f[1], f[3]);
+                        } else {                           // word 2 t + i: groups 2 i and 2 i + 1
+                            s2[0] = scale2(f[0], f[1]);
+                            s2[1] = scale2(f[2], f[3]);
+                        }
+                    }
+                    // piece of the operand row: keys in word order; values so that a 64-channel slab is hh
+                    uint8_t* const out = dst + r * 128;
+#pragma unroll
+                    for (int w4 = 0; w4 < WORDS / 8; ++w4) {
+                        const int at = part * (WORDS / 8) + w4;
+                        const uint4 w = *reinterpret_cast<const uint4*>(codes + 4 * at);
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            if ((u4[i] & 0x7f80u) == 0x7f80u) { bits |= 1u << (2 * i); u4[i] &= 0xffff0000u; }
-                            if ((u4[i] & 0x7f800000u) == 0x7f800000u) { bits |= 2u << (2 * i); u4[i] &= 0xffffu; }
+                            const int wi = 4 * at + i;
+                            uint4 o;
+                            int c;
+                            if constexpr (D == 128) {
+                                o = unpack8(ws[i], s2[i], s2[i]);
+                                c = isv ? (i & 1) * 8 + (wi >> 1) : wi;
+                            } else {
+                                o = isv ? unpack8(ws[i], s2[0], s2[1]) : unpack8(ws[i], s2[i & 1], s2[i & 1]);
+                                c = wi;
+                            }
+                            *reinterpret_cast<uint4*>(out + (c >> 3) * kSlab + (((c & 7) ^ (r & 7)) << 4)) = o;
                         }
-                        sh.bad[T & 3][(h & 1) * kHalf + ut / CH + k * (128 / CH)][c] = uint8_t(bits);
-                        if (bits) *at = make_uint4(u4[0], u4[1], u4[2], u4[3]);
-                        found |= bits != 0;
                     }
-                    found = __any_sync(0xffffffffu, found);
-                    if (lane == 0) sh.any_bad[T & 3][h & 1][warp - 12] = found;
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) arrive(isv ? &sh.v_full[T & 1] : &sh.k_full[T & 1]);
-            };
-            int pid = page_of(0), h = 0;
-            for (; h < steps; ++h) {
-                const uint32_t T = base + uint32_t(h >> 1);
-                const int n = a * kKeys + h * kHalf + lane * R;
-                int rows = lane < runs ? min(max(lim - n, 0), R) : 0;
-                long long off = rows > 0 ? paged_row(p.kv, pid, g, n) : -1;
-                if (rows > 0 && off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
-                if (off < 0) off = rows = 0;
-                pid = page_of(h + 1);
-                if ((h & 1) == 0 && T >= 2 &&              // the tile two back has been read
-                    !__all_sync(0xffffffffu, wait(isv ? &sh.v_empty[T & 1] : &sh.k_empty[T & 1], ((T >> 1) - 1) & 1)))
-                    break;
-                if (warp == 8) {                           // tokens of the step that exist
-                    const unsigned long long m =
-                        rows > 0 ? (rows >= 64 ? ~0ull : (1ull << rows) - 1) << (lane * R & 63) : 0ull;
-                    const uint32_t m0 = __reduce_or_sync(0xffffffffu, uint32_t(m));
-                    const uint32_t m1 = __reduce_or_sync(0xffffffffu, uint32_t(m >> 32));
+                    fence_async_smem();
+                    __syncwarp();
                     if (lane == 0) {
-                        sh.valid[T & 3][2 * (h & 1)] = m0;
-                        sh.valid[T & 3][2 * (h & 1) + 1] = m1;
+                        arrive(&sh.raw_empty[slot]);
+                        arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
                     }
-                }
-#pragma unroll
-                for (int k = 0; k < PER; ++k) {
-                    const int tok = ut / CH + k * (128 / CH), run = tok >> rsh, i = tok & (R - 1);
-                    const long long o = __shfl_sync(0xffffffffu, off, run);
-                    const bool there = i < __shfl_sync(0xffffffffu, rows, run);
-                    const uint8_t* const src = p.kv.data + (there ? o + i * (4 * D) + (isv ? 2 * D : 0) + c * 16 : 0);
-                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(place(h, k))), "l"(src),
-                                 "r"(there ? 16 : 0)       // (zeros where there is no token)
-                                 : "memory");
-                }
-                asm volatile("cp.async.commit_group;\n" ::: "memory");
-                if (h >= 2) {
-                    asm volatile("cp.async.wait_group 2;\n" ::: "memory");
-                    finish(h - 2);
-                }
-            }
-            asm volatile("cp.async.wait_group 0;\n" ::: "memory");
-            if (h == steps) {
-                finish(h - 2);                             // (steps is even)
-                finish(h - 1);
-            }
-            __syncwarp();
-        } else if (INT4 && warp >= 8 && warp < 8 + kUnpack) {
-            // ================================================================ unpacking
-            // Keys and values have their own warps, which meet only at the raw rows, three steps deep.
-            const bool isv = warp >= 12;
-            const int ut = (tid - 256) & 127, part = ut >> 6, tok = ut & 63;
-            constexpr int ROWB = SH::ROWB;
-            const int steps = 2 * nt;
-            for (int h = 0; h < steps; ++h) {
-                const uint32_t T = base + uint32_t(h >> 1);        // tile over the kernel
-                const int stage = T & 1, half = h & 1;
-                const uint32_t S = base_raw + uint32_t(h), slot = S % 3;
-                if (!__all_sync(0xffffffffu, wait(&sh.raw_full[slot], (S / 3) & 1))) break;
-                const uint8_t* raw = sh.raw[slot];
-                // powers of two: the largest scale (that is a number) of the 64 tokens to [2^15, 2^16)
-                auto top = [](uint32_t w) -> uint32_t { return max(w & 0x7fffu, (w >> 16) & 0x7fffu); };   // of two bf16
-                uint32_t kmx, vmx;
-                {
-                    const uint4 s0 = *reinterpret_cast<const uint4*>(raw + lane * ROWB + D);
-                    const uint4 s1 = *reinterpret_cast<const uint4*>(raw + (lane + 32) * ROWB + D);
-                    kmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.x, s0.y), max_bf16x2(s1.x, s1.y)), 0u));
-                    vmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.z, s0.w), max_bf16x2(s1.z, s1.w)), 0u));
-                    if (isv) kmx = 0;                      // (only the first key warp needs both)
-                    else if (warp != 8) vmx = 0;
-                }
-                auto expo = [](uint32_t m) { return min(max(int(m >> 7) - 127, -70), 127) - 15; };
-                const uint8_t* row = raw + tok * ROWB;
-                const uint4 all = *reinterpret_cast<const uint4*>(row + D);
-                // A tile that some queries do not see whole: every token has its own powers of two, so that what a
-                // query does not see cannot push what it sees out of fp16's range.
-                const bool edge = (a + (h >> 1) + 1) * kKeys > lim0;
-                int ek, ev;
-                if (edge) {
-                    ek = expo(top(max_bf16x2(max_bf16x2(all.x, all.y), 0u)));
-                    ev = expo(top(max_bf16x2(max_bf16x2(all.z, all.w), 0u)));
-                    if (!isv && part == 0) {
-                        sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
-                        sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
-                    }
-                } else {
-                    ek = isv ? 0 : expo(__reduce_max_sync(0xffffffffu, kmx));
-                    ev = isv || warp == 8 ? expo(__reduce_max_sync(0xffffffffu, vmx)) : 0;
-                    if (!isv && ut == 0) {
-                        sh.ek[T & 3][half] = ek;
-                        sh.ev[T & 3][half] = ev;
-                    }
-                }
-                const uint2 sc = isv ? make_uint2(all.z, all.w) : make_uint2(all.x, all.y);
-                const float mul = pow2i(isv ? -ev : -ek);
-                float f[4] = {bf_lo(sc.x) * mul, bf_hi(sc.x) * mul, bf_lo(sc.y) * mul, bf_hi(sc.y) * mul};
-                const int r = half * kHalf + tok;      // row of the operand tile
-                if (isv && edge) {
-                    // Tokens that some of the unit's queries do not see: a group that is not finite is taken as 0
-                    // (0 * NaN would reach every query) and noted for those that do see it.
-                    const int n = (a + (h >> 1)) * kKeys + r;
-#pragma unroll
-                    for (int gr = 0; gr < 4; ++gr) {
-                        const bool nan = n < lim && !(fabsf(f[gr]) <= 3.402823466e38f);
-                        const uint32_t m = __ballot_sync(0xffffffffu, nan);
-                        if (lane == 0 && part == 0) sh.poison[T & 3][gr][r >> 5] = m;
-                        if (nan) f[gr] = 0.f;
-                    }
-                }
-                if (!isv && part == 0 && lane == 0) sh.valid[T & 3][r >> 5] = sh.raw_valid[slot][tok >> 5];
-                if (half == 0 && T >= 2) {             // the tile two back has been read
-                    if (!__all_sync(0xffffffffu,
-                                    wait(isv ? &sh.v_empty[stage] : &sh.k_empty[stage], ((T >> 1) - 1) & 1)))
-                        break;
-                }
-                uint8_t* dst = isv ? sh.v[stage] : sh.k[stage];
-                const uint32_t* codes = reinterpret_cast<const uint32_t*>(row + (isv ? D / 2 : 0));
-                // scale pairs of a word's code pairs (0,4) (1,5) and (2,6) (3,7), for the words that differ in them
-                Scale2 s2[4];
-                if (D == 128) {
-                    if (isv) {                         // word 2 r + hh: groups 2 hh and 2 hh + 1
-                        s2[0] = s2[2] = scale2(f[0], f[1]);
-                        s2[1] = s2[3] = scale2(f[2], f[3]);
-                    } else {                           // word 4 t + g: group g
-#pragma unroll
-                        for (int gr = 0; gr < 4; ++gr) s2[gr] = scale2(f[gr], f[gr]);
-                    }
-                } else {
-                    if (isv) {                         // word r: groups 0 and 2, then 1 and 3
-                        s2[0] = scale2(f[0], f[2]);
-                        s2[1] = scale2(f[1], f[3]);
-                    } else {                           // word 2 t + i: groups 2 i and 2 i + 1
-                        s2[0] = scale2(f[0], f[1]);
-                        s2[1] = scale2(f[2], f[3]);
-                    }
-                }
-                // piece of the operand row: keys in word order; values so that a 64-channel slab is hh
-                uint8_t* const out = dst + r * 128;
-#pragma unroll
-                for (int w4 = 0; w4 < WORDS / 8; ++w4) {
-                    const int at = part * (WORDS / 8) + w4;
-                    const uint4 w = *reinterpret_cast<const uint4*>(codes + 4 * at);
-                    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int wi = 4 * at + i;
-                        uint4 o;
-                        int c;
-                        if constexpr (D == 128) {
-                            o = unpack8(ws[i], s2[i], s2[i]);
-                            c = isv ? (i & 1) * 8 + (wi >> 1) : wi;
-                        } else {
-                            o = isv ? unpack8(ws[i], s2[0], s2[1]) : unpack8(ws[i], s2[i & 1], s2[i & 1]);
-                            c = wi;
-                        }
-                        *reinterpret_cast<uint4*>(out + (c >> 3) * kSlab + (((c & 7) ^ (r & 7)) << 4)) = o;
-                    }
-                }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    arrive(&sh.raw_empty[slot]);
-                    arrive(isv ? &sh.v_full[stage] : &sh.k_full[stage]);
                 }
             }
         } else if (warp == 8 + kUnpack || warp == 8 + kUnpack + 1) {
