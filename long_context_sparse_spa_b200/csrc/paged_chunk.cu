@@ -5,7 +5,9 @@
 // Per 128 cached tokens and row tile, 4-bit rows:
 //   S = Q K^T        fp16 x fp16, fp32 in TMEM; K = scale * (code - 8) has at most 8 + 3 significant bits,
 //                    so it is exact in fp16 once a power of two per 64 tokens (per token where some queries
-//                    do not see all of them) brings the scales into range;
+//                    do not see all of them, or where their scales lie more than 2^11 apart) brings the scales
+//                    into range; a group whose scale is below 2^-11 of its own token's largest is off by up to
+//                    2^-19 of that largest;
 //                    Q is scaled by a power of two per row (exact above 2^-24 of the row's largest channel)
 //   P = 2^(logit + log2(V's power of two) - reference) in fp16, at most 2^15, from registers to TMEM over S
 //   O += P V         P as the TMEM operand, V exact in fp16 like K; fp32 in TMEM
@@ -51,6 +53,7 @@ constexpr int kChunkUnits = 256;          // sequences of a launch: 4 bytes of s
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kBase = 9.f, kSlack = 6.f;
+constexpr int kSpread = 11;               // powers of two over which scales in the same units are exact
 constexpr uint32_t kSpin = 1u << 22;
 
 template <int D, bool INT4>
@@ -66,8 +69,8 @@ struct ChunkShared {
     uint32_t raw_valid[3][2];                          // tokens of the step that exist
     uint64_t s_full[2], p_full[2][2], pv_half[2];      // by row tile (and half of the tokens)
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], o_done, q_full;
-    int ek[4][2], ev[4][2];                            // the powers of two of tile t (slot t % 4), by half
-    alignas(16) int8_t ek1[4][kKeys];                  // ... of a tile that not all queries see whole: by token
+    alignas(16) uint32_t pw[4][4];                     // the powers of two of tile t (slot t % 4) by 32 tokens: power_word
+    alignas(16) int8_t ek1[4][kKeys];                  // ... by token
     alignas(16) int8_t ev1[4][kKeys];
     uint32_t poison[4][4][4];                          // 4-bit, tile t: tokens whose values of group g are not finite
     // bf16, tile t (one that not all queries see whole): by token, a bit for each channel whose value is not finite,
@@ -158,8 +161,9 @@ __device__ __forceinline__ Scale2 scale2(float a, float b) {
 }
 // Eight codes of a word as (u - 8) s, in the order 0 4 1 5 2 6 3 7.  A code in bits 3-6 is the fp16
 // denormal u * 2^-21, in bits 7-10 u * 2^-17 (bit 10 is the exponent's lowest, whose step is the denormals'):
-// even codes come times 2^-21, odd ones times 2^-17.  (u - 8) s has at most 3 + 8 bits, so with s up to 2^16
-// the result is exact for scales down to 2^-9 of that, and below within 2^-23 of the largest value.
+// even codes come times 2^-21, odd ones times 2^-17.  (u - 8) s has at most 3 + 8 bits, the lowest of them
+// 2^-7 of s's power of two; with that power at least 2^4 it is not below 2^-24, fp16's last place, and the result
+// is exact.  The largest scale has 2^15, so scales may lie 2^kSpread apart; a smaller one is off by up to 2^-4.
 __device__ __forceinline__ uint4 unpack8(uint32_t w, const Scale2& a, const Scale2& b) {
     const uint32_t x = w << 3, y = w >> 5;
     return make_uint4(fma_f16x2(x & 0x00780078u, a.s, a.lo), fma_f16x2(x & 0x07800780u, a.s, a.hi),
@@ -189,6 +193,20 @@ __device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b) {
     return r;
 }
 
+// Whether one of four bf16 scales is not zero and its bits are at most `limit` (the same in both halves): less one as
+// 16-bit integers, zeros are the largest (NaNs are above any scale).
+__device__ __forceinline__ bool any_below(uint32_t a, uint32_t b, uint32_t limit) {
+    uint32_t m;
+    asm("{\n .reg .b32 x, y;\n add.u16x2 x, %1, %3;\n add.u16x2 y, %2, %3;\n min.u16x2 x, x, y;\n min.u16x2 %0, x, %4;\n}\n"
+        : "=r"(m)
+        : "r"(a), "r"(b), "r"(0xffffffffu), "r"(limit));
+    return m != limit;
+}
+// the powers of two of 64 tokens' keys and values, and whether 32 of them have their own instead
+__device__ __forceinline__ uint32_t power_word(int ek, int ev, bool own) {
+    return (uint32_t(ek) & 0xffu) | (uint32_t(ev) & 0xffu) << 8 | (own ? 1u << 16 : 0u);
+}
+
 // floats of one share of a split unit: O [D / 4][256][4], then m, l and four words of poisoned groups (4-bit: the
 // first) or channels of each row
 __host__ __device__ constexpr int chunk_rec_floats(int d) { return 256 * (d + 6); }
@@ -215,7 +233,7 @@ __device__ __forceinline__ long long head_weight(const SeqG& s, int TQ) {
 template <int D, bool INT4>
 __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
     using SH = ChunkShared<D, INT4>;
-    static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && SH::ROWB % 16 == 0 && offsetof(SH, ek1) % 16 == 0 &&
+    static_assert(offsetof(SH, valid) % 16 == 0 && offsetof(SH, pw) % 16 == 0 && offsetof(SH, raw) % 16 == 0 && SH::ROWB % 16 == 0 && offsetof(SH, ek1) % 16 == 0 &&
                   sizeof(SH) % 8 == 0, "alignment of shared accesses");
     constexpr int NW = INT4 ? 1 : D / 32;              // words of poisoned groups or channels
     constexpr int WORDS = D / 8;                       // 16-byte pieces of an operand row, code words of a row
@@ -485,30 +503,37 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                         const uint4 s1 = *reinterpret_cast<const uint4*>(raw + (lane + 32) * ROWB + D);
                         kmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.x, s0.y), max_bf16x2(s1.x, s1.y)), 0u));
                         vmx = top(max_bf16x2(max_bf16x2(max_bf16x2(s0.z, s0.w), max_bf16x2(s1.z, s1.w)), 0u));
-                        if (isv) kmx = 0;                      // (only the first key warp needs both)
-                        else if (warp != 8) vmx = 0;
+                        if (isv) kmx = 0;                      // (only the key warps of part 0 need both)
+                        else if (part) vmx = 0;
                     }
                     auto expo = [](uint32_t m) { return min(max(int(m >> 7) - 127, -70), 127) - 15; };
                     const uint8_t* row = raw + tok * ROWB;
                     const uint4 all = *reinterpret_cast<const uint4*>(row + D);
                     // A tile that some queries do not see whole: every token has its own powers of two, so that what a
-                    // query does not see cannot push what it sees out of fp16's range.
+                    // query does not see cannot push what it sees out of fp16's range.  So have the 32 tokens of a warp
+                    // where one has a scale too far below the 64 tokens' largest to be exact in its units: a token of
+                    // large keys or values and little weight must not blur the others.  (Keys and values each by
+                    // themselves; the warps of both parts find the same.)
                     const bool edge = (a + (h >> 1) + 1) * kKeys > lim0;
-                    int ek, ev;
-                    if (edge) {
-                        ek = expo(top(max_bf16x2(max_bf16x2(all.x, all.y), 0u)));
-                        ev = expo(top(max_bf16x2(max_bf16x2(all.z, all.w), 0u)));
-                        if (!isv && part == 0) {
-                            sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
-                            sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
+                    int ek = 0, ev = 0;
+                    bool kown = edge, vown = edge;
+                    if (!edge) {
+                        auto below = [](int e) { return uint32_t(((e + 15 + 127 - kSpread) << 7) - 1) * 0x10001u; };
+                        if (!isv) {
+                            ek = expo(__reduce_max_sync(0xffffffffu, kmx));
+                            kown = __any_sync(0xffffffffu, any_below(all.x, all.y, below(ek)));
                         }
-                    } else {
-                        ek = isv ? 0 : expo(__reduce_max_sync(0xffffffffu, kmx));
-                        ev = isv || warp == 8 ? expo(__reduce_max_sync(0xffffffffu, vmx)) : 0;
-                        if (!isv && ut == 0) {
-                            sh.ek[T & 3][half] = ek;
-                            sh.ev[T & 3][half] = ev;
+                        if (isv || part == 0) {
+                            ev = expo(__reduce_max_sync(0xffffffffu, vmx));
+                            vown = __any_sync(0xffffffffu, any_below(all.z, all.w, below(ev)));
                         }
+                    }
+                    if (!isv && part == 0 && lane == 0) sh.pw[T & 3][(half * kHalf + tok) >> 5] = power_word(ek, ev, kown || vown);
+                    if (kown) ek = expo(top(max_bf16x2(max_bf16x2(all.x, all.y), 0u)));
+                    if (vown) ev = expo(top(max_bf16x2(max_bf16x2(all.z, all.w), 0u)));
+                    if (!isv && part == 0) {
+                        sh.ek1[T & 3][half * kHalf + tok] = int8_t(ek);
+                        sh.ev1[T & 3][half * kHalf + tok] = int8_t(ev);
                     }
                     const uint2 sc = isv ? make_uint2(all.z, all.w) : make_uint2(all.x, all.y);
                     const float mul = pow2i(isv ? -ev : -ek);
@@ -822,15 +847,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 const int n0 = n0_of(t);
                 const uint4 vd = *reinterpret_cast<const uint4*>(sh.valid[T & 3]);
                 const uint32_t vm[4] = {vd.x, vd.y, vd.z, vd.w};
-                const bool edge = n0 + kKeys > lim0, gaps = (vm[0] & vm[1] & vm[2] & vm[3]) != 0xffffffffu;
+                bool edge = n0 + kKeys > lim0;
+                const bool gaps = (vm[0] & vm[1] & vm[2] & vm[3]) != 0xffffffffu;
                 const int seen = lim_r - n0;               // columns below this one are seen
                 float cs[2] = {hrow, hrow}, ev[2] = {0.f, 0.f};
-                if (INT4 && !edge) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        cs[h] = hrow * pow2i(sh.ek[T & 3][h]);
-                        ev[h] = float(sh.ev[T & 3][h]);
-                    }
+                if constexpr (INT4) {
+                    const uint4 pw = *reinterpret_cast<const uint4*>(sh.pw[T & 3]);
+                    edge |= (pw.x | pw.y | pw.z | pw.w) >> 16 != 0;    // powers of two by token
+                    cs[0] = hrow * pow2i(int8_t(pw.x));
+                    cs[1] = hrow * pow2i(int8_t(pw.z));
+                    ev[0] = float(int8_t(pw.x >> 8));
+                    ev[1] = float(int8_t(pw.z >> 8));
                 }
                 // logits + V's power of two of 32 tokens, for tiles with tokens that are not seen or do not exist
                 auto masked = [&](int q4, float (&v)[32]) {
@@ -848,9 +875,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const int i = 4 * i4 + k;
-                            const float c = edge ? hrow * pow2i(ee[k]) : q4 < 2 ? cs[0] : cs[1];
-                            const float o = edge ? float(ff[k]) : q4 < 2 ? ev[0] : ev[1];
-                            v[i] = ((vm[q4] >> i) & 1u) && q4 * 32 + i < seen ? fmaf(v[i], c, o) : -INFINITY;
+                            v[i] = ((vm[q4] >> i) & 1u) && q4 * 32 + i < seen
+                                       ? fmaf(v[i], hrow * pow2i(ee[k]), float(ff[k]))
+                                       : -INFINITY;
                         }
                     }
                 };
@@ -945,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             v[i] = ex2_approx(v[i] + ref);
-                            const int e = edge ? sh.ev1[T & 3][q4 * 32 + i] : sh.ev[T & 3][q4 >> 1];
+                            const int e = sh.ev1[T & 3][q4 * 32 + i];
                             l = fmaf(v[i], pow2i(-e), l);
                         }
 #pragma unroll
