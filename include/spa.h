@@ -561,8 +561,11 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
  *   out [T, Hq, d] bf16, out_f32 [T, Hq, d] fp32 (optional), both 16-byte aligned as ws is;
  *   lse [T, Hq] fp32 (optional).
  * A query that sees nothing gives out = 0 and lse = -inf.  Weights are carried in 11 bits (4-bit
- * cache: fp16 against exact codes) or about 16 (bf16 cache), sums in binary32.  What a
- * query does not see does not reach it, values that are not finite included.
+ * cache: fp16) or about 16 (bf16 cache), sums in binary32.  4-bit values enter as they are (scale *
+ * (code - 8), exactly), except that those of a group whose scale is below 2^-11 of the largest of
+ * its token's four are off by up to 2^-19 of that largest, and all by up to 2^-89 (keys too in
+ * calls with more than 32 rows, a query of a head each, per sequence and kv head on average).
+ * What a query does not see does not reach it, values that are not finite included.
  * Hq / Hkv <= 16; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(a);
  * a workspace serves calls of the same arguments but for the pointers' values. */
 typedef struct spa_paged_attend_args {

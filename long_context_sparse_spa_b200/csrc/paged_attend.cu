@@ -15,11 +15,12 @@
 //     fp16's range (and by 1/16 for the second kind), exactly above 2^-24 of its largest channel; the
 //     group scale multiplies in fp32, and the -8 terms are one more product, scales times three bf16
 //     terms of the sums.
-//   4-bit values: with r_g = s_g / (the token's largest s) and P = p * (that largest s), both in fp16 (11
-//     bits), O += V^T P^T with V = (u - 8) r_g, one fp16 FMA per two codes after the AND.  A transposing
-//     ldmatrix over 16-bit units (four codes of a token) pairs tokens for the A operand.  So that P fits
-//     fp16 whatever the scales are, the running reference of the softmax is the maximum of (logit + log2 of
-//     the token's largest value scale), not of the logit; P <= 2^15, and l = sum p is kept in fp32.
+//   4-bit values: with 2^e the power of two of the token's largest s, r_g = s_g 2^-e and P = p 2^e, O += V^T P^T
+//     with V = (u - 8) r_g, one fp16 FMA per two codes after the AND.  V has 3 + 8 bits and is exact (a group's
+//     scale below 2^-11 of its token's largest: within 2^-19 of that); only the weight is rounded, to fp16's 11
+//     bits, half a step of the outputs' bf16 / 8.  A transposing ldmatrix over 16-bit units (four codes of a
+//     token) pairs tokens for the A operand.  So that P fits fp16 whatever the scales are, the running reference
+//     of the softmax is the maximum of (logit + e), not of the logit; P <= 2^15, and l = sum p is kept in fp32.
 //   bf16 rows: S = K Q^T, O += V^T P^T with P = hi + lo bf16 (about 16 bits).
 // The m16 rows of a tile are a permutation of its tokens (tau) that keeps the shared-memory reads free
 // of bank conflicts for the rows' strides; a softmax does not see the order.
@@ -47,7 +48,7 @@ constexpr int kSeg = 32;                  // tiles charged to a unit for its sta
 constexpr int kShare = 16;                // least weighted tiles of a CTA's share
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kFloorV = 8.077935669463161e-28f;   // 2^-90: least value scale that the reference follows
+constexpr float kFloorV = 8.077935669463161e-28f;   // 2^-90: least value scale that the reference follows (l = sum P / 2^e)
 constexpr float kBase = 9.f;              // weights are 2^9 at the reference, and at most 2^(9 + kSlack)
 constexpr float kSlack = 6.f;             // the reference moves only when it is exceeded by this (log2)
 constexpr uint32_t kWaitLimit = 1u << 22;
@@ -72,18 +73,13 @@ struct Geo {
     static constexpr int RING = WARPS * STAGES * TILE * SROW;
     // the warps' parts, their factors and (M, L); the merge of shares puts a factor of each over the parts
     static constexpr int MERGE = WARPS * NT * 8 * (D + 2) * 4 + NT * 8 * (WARPS + 2) * 4;
-    static constexpr int PREP = INT4 ? WARPS * TILE * 8 : 0;   // (log2, 1 / value) of each token's largest value scale
+    static constexpr int PREP = INT4 ? WARPS * TILE * 8 : 0;   // (e, 2^-e) of each token's largest value scale
     static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + PREP + QBYTES;
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float bf_lo(uint32_t x) { return __uint_as_float(x << 16); }
@@ -684,15 +680,16 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                 poison = __any_sync(0xffffffffu, poison);
             }
             if constexpr (INT4) {
-                // One token per lane: its largest value scale that is a number (its bits twice: at most 2^-7 more),
-                // log2 and 1 / of it, and the scales relative to it as fp16 * 2^15, stored by token pairs over the
-                // scales themselves.
+                // One token per lane: the power of two 2^e of its largest value scale that is a number, and the scales
+                // times 2^-e (in [0, 2)) as fp16 * 2^15, exactly above 2^-32, stored by token pairs over the scales
+                // themselves.
                 const uint32_t row = st + lane * SROW + D + 8;
                 const uint2 v = lds64(row);
-                const uint32_t m2 = max_bf16x2(v.x, v.y);
-                const float top = fmaxf(__uint_as_float(max_bf16x2(m2, __byte_perm(m2, m2, 0x1032))), kFloorV);
+                const uint32_t m2 = max_bf16x2(max_bf16x2(v.x, v.y), 0u);
+                const uint32_t m = max_bf16x2(m2, __byte_perm(m2, m2, 0x1032));
+                const float top = fmaxf(__uint_as_float(m & 0x7f800000u), kFloorV);
                 const float iv = __frcp_rn(top);
-                sts64(prep + lane * 8, __float_as_uint(lg2(top)), __float_as_uint(iv));
+                sts64(prep + lane * 8, __float_as_uint(float(int(__float_as_uint(top) >> 23) - 127)), __float_as_uint(iv));
                 const uint32_t h01 = pack_f16(bf_lo(v.x) * iv * 32768.f, bf_hi(v.x) * iv * 32768.f);
                 const uint32_t h23 = pack_f16(bf_lo(v.y) * iv * 32768.f, bf_hi(v.y) * iv * 32768.f);
                 // rows 2i and 2i + 1 of a 16-row tile are a pair; the partner's token
@@ -781,7 +778,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
                         }
                     }
                 }
-                // ---- the reference follows logit + log2 of the value scale
+                // ---- the reference follows logit + the value scale's e
                 bool up = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -891,7 +888,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
 #pragma unroll
                             for (int e = 0; e < 2; ++e) {       // codes 2e and 2e + 1 of the units
                                 // a code in bits 3-6 is u * 2^-21 as fp16, in bits 7-10 u * 2^-17 (bit 10 is the
-                                // exponent's lowest, whose step is the denormals'): products stay above 2^-6 r
+                                // exponent's lowest, whose step is the denormals'): products stay above 2^-6 r, exact
                                 const uint32_t lo = e ? x[2 * q] >> 5 : x[2 * q] << 3;
                                 const uint32_t hi = e ? x[2 * q + 1] >> 5 : x[2 * q + 1] << 3;
                                 const int i = NG == 1 ? 0 : e;

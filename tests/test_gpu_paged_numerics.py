@@ -89,3 +89,26 @@ def test_tokens_of_large_keys_or_values_and_little_weight(d, new, where, ke, ve)
     for i in sorted({0, new // 2, new - 1}):
         check_closely(c, _bf(q)[i], _np(plan.out_f32)[i].astype(np.float64), _np(plan.lse)[i].astype(np.float64),
                       np.arange(L) <= L - new + i, scale, 0, f"query {i}")
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("L,new", [(1, 1), (40, 1), (40, 2), (33, 5)])
+def test_values_of_equal_tokens_come_back_exactly(d, L, new):
+    # all tokens of a sequence are the same: weights are equal, in the units of the softmax a power of two, and the output
+    # is the 4-bit value itself up to binary32 (the reference's and the logit's rounding, 2^-18, and the accumulation)
+    B = 6
+    c = Cache([L] * B, 1, d, 16, INT4, seed=62)
+    rng = np.random.default_rng(62)
+    for b in range(B):
+        k, v = rng.standard_normal((2, d))
+        v *= np.repeat(2.0 ** rng.integers(-9, 2, 4), d // 4)       # groups of different sizes, and of zeros
+        v[: d // 4] *= b != 3
+        for n in range(L):
+            put(c, b, n, k, v)
+    q = torch.randn(B * new, 4, d, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32(np.arange(B + 1) * new), want_f32=True, **c.kw)
+    out = _np(plan.out_f32).astype(np.float64)
+    for t in range(B * new):
+        v = c.V[t // new][0, 0]
+        err = np.abs(out[t] - v)
+        assert (err <= np.abs(v) * (2.0**-18 + L * 2.0**-23)).all(), f"row {t}: off by {(err / np.abs(v).max()).max():.2e}"
