@@ -492,7 +492,10 @@ spa_status spa_pbs_prefill_timed(const spa_pbs_args* a, void* ws, size_t ws_byte
  * would be written to stays as it is.  NULL: one new token per sequence, T = B.
  * Device-side conditions raise (1 << SPA_ERR_INVALID_ARG) in the status word at the head of
  * ws: a page number outside [0, num_pages), a length outside [0, max_pages * page], a sequence
- * start out of order.  A token on a bad page is neither written nor attended to.
+ * whose rows are not 0 <= seq_start[b] <= seq_start[b + 1] <= T, a token appended before the first
+ * (kv_len[b] below the number of new tokens) or gathered from before it (start[b] < 0).  A token on
+ * a bad page is neither written nor attended to; a sequence with such rows has no new tokens.  A
+ * row that several sequences name (starts out of order again) is appended to one of them.
  */
 typedef enum spa_kv_format { SPA_KV_BF16 = 0, SPA_KV_INT4 = 1 } spa_kv_format;
 

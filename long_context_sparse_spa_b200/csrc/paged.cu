@@ -19,6 +19,8 @@
 // Measured on B200: append of 4096 tokens (32 query, 8 kv heads, d = 128) in 4 bits about 33 us and 8 us for reading
 // them back, 88 + 22 MB; bound by instruction issue (rotation and quantisation of 16-byte pieces).  Gather of 28672
 // 4-bit tokens of 8 heads to bf16 (150 MB) 28.7 us, 5.2 TB/s, bound by memory and shared memory together.
+#include <climits>
+
 #include "paged.cuh"
 
 namespace spa {
@@ -97,17 +99,27 @@ __global__ void __launch_bounds__(kThreads, kAppCtas) paged_append_kernel(PagedA
         ahead[i] = fetch(next);
         step(next);
     }
+    // starts out of order are reported once (by the warps, if there are any, that look up no token)
+    if (p.seq_start && blockIdx.x == 0)
+        for (int k = kThreads - 1 - tid; k < p.kv.B; k += kThreads)
+            if (!paged_rows_ok(p.seq_start[k], p.seq_start[k + 1], p.T)) raise_status(p.status, SPA_ERR_INVALID_ARG);
     if (tid < 32 * nt) {                    // a warp per token
         const int lane = tid & 31, i = tid >> 5, t = t0 + i;
-        int b;
-        if (p.seq_start && p.kv.B <= 1024) {
-            // the sequence by counting the starts at or before t: the loads do not wait for one another
-            int n = 0;
-            for (int k = lane; k <= p.kv.B; k += 32) n += p.seq_start[k] <= t ? 1 : 0;
-            b = __reduce_add_sync(0xffffffffu, n) - 1;
-            if (b >= p.kv.B || b < 0 || p.seq_start[b] > t || t >= p.seq_start[b + 1]) b = -1;
-        } else {
+        int b = -1;
+        if (!p.seq_start || p.kv.B > 1024) {
             b = paged_seq_of(p.seq_start, p.kv.B, t);
+            if (b >= 0 && p.seq_start && !paged_rows_ok(p.seq_start[b], p.seq_start[b + 1], p.T)) b = -1;
+        }
+        if (b < 0 && p.seq_start) {
+            // the first sequence that the attention too takes the row for (the loads do not wait for one another; many
+            // starts only where they are out of order, or for a row of nobody)
+            int first = INT_MAX;
+            for (int k = lane; k < p.kv.B; k += 32) {
+                const int a = p.seq_start[k], e = p.seq_start[k + 1];
+                if (a <= t && t < e && paged_rows_ok(a, e, p.T)) first = min(first, k);
+            }
+            first = __reduce_min_sync(0xffffffffu, first);
+            if (first < INT_MAX) b = first;
         }
         if (lane == 0) {
             long long row = -1;

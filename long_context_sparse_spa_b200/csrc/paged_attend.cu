@@ -166,7 +166,7 @@ __device__ __forceinline__ SeqGeo seq_geo(const PagedAttendParams& p, int b, boo
         s.row0 = b;
     } else {
         const long long a = p.seq_start[b], e = p.seq_start[b + 1];
-        if (a < 0 || e > p.T || e < a) { *bad = true; s.n = 0; s.row0 = 0; }
+        if (!paged_rows_ok(a, e, p.T)) { *bad = true; s.n = 0; s.row0 = 0; }
         else { s.n = int(e - a); s.row0 = int(a); }
     }
     return s;
@@ -176,7 +176,7 @@ __device__ __forceinline__ SeqGeo seq_geo(const PagedAttendParams& p, int b, boo
 __device__ __forceinline__ int one_row(const PagedAttendParams& p, int b, bool* bad) {
     if (!p.seq_start) return b;
     const int a = p.seq_start[b], e = p.seq_start[b + 1];
-    if (a >= 0 && e <= p.T && (long long)e - a == 1) return a;
+    if (paged_rows_ok(a, e, p.T) && e - a == 1) return a;
     if (e != a) *bad = true;
     return -1;
 }

@@ -216,7 +216,7 @@ __device__ __forceinline__ SeqG seq_geo(const PagedAttendParams& p, int b, bool*
     SeqG s;
     s.len = paged_len(p.kv, p.kv.kv_len[b], bad);
     const long long a = p.seq_start[b], e = p.seq_start[b + 1];
-    if (a < 0 || e > p.T || e < a) { *bad = true; s.n = 0; s.row0 = 0; }
+    if (!paged_rows_ok(a, e, p.T)) { *bad = true; s.n = 0; s.row0 = 0; }
     else { s.n = int(e - a); s.row0 = int(a); }
     return s;
 }

@@ -47,6 +47,9 @@ SPA_HD long long paged_row(const PagedView& v, int pid, int g, long long n) {
     return ((((long long)pid * v.Hkv + g) << v.page_shift) + in_page) * v.row_bytes;
 }
 
+// whether [a, e), a sequence's start and the next one's, are rows of T; where not, the sequence has no new tokens
+SPA_HD bool paged_rows_ok(long long a, long long e, int T) { return a >= 0 && a <= e && e <= T; }
+
 // sequence whose rows [seq_start[b], seq_start[b + 1]) hold token t, or -1 (rows before the first or
 // behind the last sequence); seq_start null: one token per sequence
 SPA_HD int paged_seq_of(const int32_t* seq_start, int B, int t) {

@@ -954,3 +954,79 @@ def test_python_refusals():
         spa.paged_attend(q=torch.zeros(2, 34, 64, dtype=torch.bfloat16, device="cuda"), sm_scale=0.1, **c.kw)
     with pytest.raises((TypeError, ValueError)):
         spa.paged_gather(N=4, K=k, **c.kw)
+
+
+def _far(B):
+    # two sequences with rows, 0-1 and 3-4, among empty ones, and a start out of order between them
+    s = np.full(B + 1, 3, np.int64)
+    s[:11], s[11], s[12], s[B] = 0, 2, -4, 5
+    return s.tolist()
+
+
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+@pytest.mark.parametrize("T,start", [(8, [0, 5, 3, 8]), (8, [-2, 3, 8]), (8, [0, 4, 12]), (8, [6, 2, 8, 1]),
+                                     (8, [-7, 2, 1 << 30, 2, 8]), (8, [0, 3, 3, -1, 4, 8]), (6, _far(40)), (6, _far(300)),
+                                     (6, _far(1500))])
+def test_append_reports_starts_out_of_order_and_keeps_to_the_other_sequences(fmt, T, start):
+    B, d = len(start) - 1, 64
+    ok = [0 <= a <= e <= T for a, e in zip(start, start[1:])]
+    lens = [e - a if g else 1 for a, e, g in zip(start, start[1:], ok)]
+    c = Cache(lens, 1, d, 16, fmt, fill=False)
+    c.pool.view(torch.uint8).fill_(0xA5)
+    kv = torch.randn(2, T, 1, d, device="cuda").to(torch.bfloat16)
+    q = torch.randn(T, 2, d, device="cuda").to(torch.bfloat16)
+    q_out = torch.full_like(q, 7)
+    add = spa.paged_append(k=kv[0], v=kv[1], q=q, q_out=q_out, seq_start=_i32(start), **c.kw)
+    assert spa.read_device_status(add.ws) == INVALID
+    host = _np(c.pool.view(torch.uint8)).reshape(c.pool.shape[0], 1, 16, -1)
+    want = np.full_like(host, 0xA5)
+    k, v = _bf(kv[0]).astype(np.float32), _bf(kv[1]).astype(np.float32)
+    shared = False
+    for t in range(T):
+        mine = [b for b in range(B) if ok[b] and start[b] <= t < start[b + 1]]
+        shared |= len(mine) > 1
+        assert torch.equal(q_out[t], q[t] if mine else torch.full_like(q[t], 7))
+        if mine:
+            n = t - start[mine[0]]
+            row = ref.pack(k[t], v[t]) if fmt == INT4 else np.concatenate(
+                (ref.bf16_bits(k[t]), ref.bf16_bits(v[t])), -1).astype("<u2").view(np.uint8)
+            want[c.table[mine[0], n // 16], :, n % 16] = row
+    assert (host == want).all()
+    if shared:
+        return
+    att = spa.paged_attend(q=q, sm_scale=0.2, seq_start=_i32(start), run=False, **c.kw)
+    att.out.fill_(9)
+    att.run()
+    assert spa.read_device_status(att.ws) == INVALID
+    if fmt == INT4:
+        k, v, ks, vs = ref.unpack(ref.pack(k[:, 0], v[:, 0]))
+    for b in range(B):
+        if ok[b] and lens[b]:
+            a, e = start[b], start[b + 1]
+            c.K, c.V = {b: k[a:e].reshape(1, e - a, d)}, {b: v[a:e].reshape(1, e - a, d)}
+            if fmt == INT4:
+                c.ks, c.vs = {b: ks[None, a:e]}, {b: vs[None, a:e]}
+            for i in range(e - a):
+                check_attention(c, _bf(q)[a + i], _bf(att.out)[a + i], _np(att.lse)[a + i].astype(np.float64),
+                                [np.arange(e - a) <= i], 0.2, b, f"sequence {b}, row {a + i}")
+    nobody = [t for t in range(T) if not any(ok[b] and start[b] <= t < start[b + 1] for b in range(B))]
+    assert (att.out[nobody] == 9).all()
+
+
+def test_append_of_many_sequences():
+    # more sequences than a warp counts through: rows of each, of empty ones, and of nobody
+    B, d = 1500, 64
+    new = [(3 * b) % 4 for b in range(B)]
+    start = np.concatenate(([0], np.cumsum(new))) + 2
+    T = int(start[-1]) + 5
+    c = Cache([max(n, 1) for n in new], 1, d, 16, INT4, fill=False)
+    c.pool.fill_(0xA5)
+    kv = torch.randn(2, T, 1, d, device="cuda").to(torch.bfloat16)
+    add = spa.paged_append(k=kv[0], v=kv[1], seq_start=_i32(start), **c.kw)
+    assert spa.read_device_status(add.ws) == 0
+    want = np.full_like(_np(c.pool), 0xA5)
+    rows = ref.pack(_bf(kv[0]).astype(np.float32), _bf(kv[1]).astype(np.float32))
+    for b in range(B):
+        for i in range(new[b]):
+            want[c.table[b, 0], :, i] = rows[start[b] + i]
+    assert (_np(c.pool) == want).all()
