@@ -90,11 +90,16 @@ const char* spa_last_cuda_error(void);
  *                               then reads the scores from global memory, so its results
  *                               stay those of a normal run;
  *   SPA_TEST_STALL_PREFILL_MMA  the tcgen05 prefill's first S = Q K^T; the CTA writes no
- *                               output and frees its tensor memory.
+ *                               output and frees its tensor memory;
+ *   SPA_TEST_STALL_PAGED_COPY   the copies of cached rows of the paged attention of up to 32 rows,
+ *   SPA_TEST_STALL_PAGED_CHUNK  the first S = Q K^T of the paged attention of more: results of that
+ *                               call are undefined, the workspace is ready for the next one.
  * Process-wide; bits = 0 restores normal launches.  Returns SPA_ERR_INVALID_ARG for unknown
  * bits.  Not for production use. */
 #define SPA_TEST_STALL_SELECT_LOAD 1
 #define SPA_TEST_STALL_PREFILL_MMA 2
+#define SPA_TEST_STALL_PAGED_COPY 8
+#define SPA_TEST_STALL_PAGED_CHUNK 16
 spa_status spa_test_stall(int bits);
 
 /* ABI version of this header: 6 (spa_decode_args gained local_units in 2, the RLA fields in 3;

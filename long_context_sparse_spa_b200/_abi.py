@@ -29,6 +29,8 @@ SPA_SELECT_TOPP = 1
 SPA_SELECT_STATIC_MAX_UNITS = 16
 SPA_TEST_STALL_SELECT_LOAD = 1
 SPA_TEST_STALL_PREFILL_MMA = 2
+SPA_TEST_STALL_PAGED_COPY = 8
+SPA_TEST_STALL_PAGED_CHUNK = 16
 SPA_DECODE_AUTO = 0
 SPA_DECODE_SEPARATE = 1
 SPA_DECODE_FUSED = 2

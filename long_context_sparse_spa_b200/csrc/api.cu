@@ -146,7 +146,9 @@ const char* spa_status_string(int s) {
 const char* spa_last_cuda_error(void) { return g_last_cuda_error.c_str(); }
 
 spa_status spa_test_stall(int bits) {
-    if (bits & ~(SPA_TEST_STALL_SELECT_LOAD | SPA_TEST_STALL_PREFILL_MMA)) return SPA_ERR_INVALID_ARG;
+    if (bits & ~(SPA_TEST_STALL_SELECT_LOAD | SPA_TEST_STALL_PREFILL_MMA | SPA_TEST_STALL_PAGED_COPY |
+                 SPA_TEST_STALL_PAGED_CHUNK))
+        return SPA_ERR_INVALID_ARG;
     g_test_stall.store(bits, std::memory_order_relaxed);
     return SPA_OK;
 }

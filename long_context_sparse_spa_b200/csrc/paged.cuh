@@ -44,6 +44,8 @@ struct PagedAttendParams {
     int* arrived;               // [CTAs]: finished shares of the split unit that starts in a CTA; 0 between calls
     float* partials;            // [2 * CTAs] shares of split units
     uint32_t* status;
+    uint32_t spin;              // tries of a bounded wait
+    int stall;                  // test hook (spa_test_stall): what a wait is for never starts
 };
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse);

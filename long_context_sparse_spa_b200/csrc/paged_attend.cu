@@ -51,7 +51,7 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kFloorV = 8.077935669463161e-28f;   // 2^-90: least value scale that the reference follows (l = sum P / 2^e)
 constexpr float kBase = 9.f;              // weights are 2^9 at the reference, and at most 2^(9 + kSlack)
 constexpr float kSlack = 6.f;             // the reference moves only when it is exceeded by this (log2)
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr uint32_t kWaitLimit = 1u << 22, kStallLimit = 1u << 10;   // tries of a wait; with the test hook
 
 // floats of one share of a split unit
 __host__ __device__ constexpr int paged_rec_floats(int d, int rows) { return rows * (d + 2); }
@@ -326,7 +326,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
     }
     const float sl2 = p.sm_scale * kLog2e;
     uint32_t phases = 0;      // parity of each stage's barrier
-    bool failed = false;      // a wait gave up: the rest of this CTA's waits are short
+    bool failed = false;      // a wait of this warp gave up: it copies nothing more
     uint8_t* const my_ring = ring + size_t(warp) * STAGES * TILE * SROW;
 
     long long x = x0;
@@ -402,7 +402,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
         const int R = 1 << rsh;
         constexpr int kTileSh = TILE == 32 ? 5 : 4;
         const int runsh = kTileSh - rsh;
-        const int n_my = a + warp < bnd ? (bnd - a - warp + kWarps - 1) / kWarps : 0;
+        const int n_my = a + warp < bnd && !failed ? (bnd - a - warp + kWarps - 1) / kWarps : 0;
         const int persh = 5 - runsh;            // tiles whose runs the lanes hold at once (a batch): lane i has run
         const int my_tile = lane >> runsh, my_run = lane & ((1 << runsh) - 1);   // my_run of the batch's tile my_tile
         // first token of this lane's run in batch k of my tiles, or -1
@@ -441,6 +441,7 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
         auto issue = [&](int j) {               // tile j of mine, which is in the batch in hand
             const int stage = fill;
             fill = fill + 1 == STAGES ? 0 : fill + 1;
+            if (p.stall) return;
             const uint32_t bar = smem_u32(&s_full[warp][stage]);
             const uint32_t dst = smem_u32(my_ring + size_t(stage) * TILE * SROW);
             const int slot = j & ((1 << persh) - 1);
@@ -632,32 +633,34 @@ paged_attend_kernel(PagedAttendParams p, int g0, int groups, int TQ) {
         }
 
         int drain = 0;
+        // bounded wait for the copies into a stage; for the whole warp
+        auto landed = [&](int stage) -> bool {
+            const uint32_t bar = smem_u32(&s_full[warp][stage]);
+            const uint32_t par = (phases >> stage) & 1u;
+            uint32_t ok = 0;
+            for (uint32_t it = 0; !ok && it < p.spin; ++it)
+                asm volatile(
+                    "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 "
+                    "%0, 1, 0, q;\n}\n"
+                    : "=r"(ok)
+                    : "r"(bar), "r"(par)
+                    : "memory");
+            return __all_sync(0xffffffffu, ok != 0);
+        };
         for (int j = 0; j < n_my; ++j) {
             advance();
             const int stage = drain;
             drain = drain + 1 == STAGES ? 0 : drain + 1;
-            {
-                const uint32_t bar = smem_u32(&s_full[warp][stage]);
-                const uint32_t par = (phases >> stage) & 1u;
-                auto poll = [&](uint32_t limit) -> bool {
-                    uint32_t ok = 0;
-                    for (uint32_t it = 0; !ok && it < limit; ++it)
-                        asm volatile(
-                            "{\n .reg .pred q;\n mbarrier.try_wait.parity.shared::cta.b64 q, [%1], %2;\n selp.u32 "
-                            "%0, 1, 0, q;\n}\n"
-                            : "=r"(ok)
-                            : "r"(bar), "r"(par)
-                            : "memory");
-                    return ok != 0;
-                };
-                if (!poll(failed ? 1024u : kWaitLimit)) {   // the copy never landed: results are undefined
-                    raise_status(p.status, SPA_ERR_TIMEOUT);
-                    if (!failed) poll(kWaitLimit);          // a last chance for what is in flight
-                    failed = true;
+            if (!landed(stage)) {               // the copy never landed: results are undefined
+                raise_status(p.status, SPA_ERR_TIMEOUT);
+                failed = true;
+                for (int k = j + 1; k < issued; ++k) {   // what else is in flight lands first, or has as long to
+                    landed(drain);
+                    drain = drain + 1 == STAGES ? 0 : drain + 1;
                 }
-                phases ^= 1u << stage;
-                __syncwarp();
+                break;
             }
+            phases ^= 1u << stage;
             const uint32_t st = smem_u32(my_ring + size_t(stage) * TILE * SROW);
             const uint32_t vmask = s_vmask[warp][stage];
             const int n0 = (a + warp + j * kWarps) * TILE;
@@ -1135,7 +1138,10 @@ void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch) {
     p.partials = reinterpret_cast<float*>(scratch + align_up(paged_attend_grid_max() * 4, 256));
 }
 
-spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st) {
+spa_status launch_paged_attend(const PagedAttendParams& args, cudaStream_t st) {
+    PagedAttendParams p = args;
+    p.stall = (test_stall_bits() & SPA_TEST_STALL_PAGED_COPY) != 0;
+    p.spin = p.stall ? kStallLimit : kWaitLimit;
     const int G = p.Hq / p.kv.Hkv;
     const int sms = device_info().num_sms;
     const bool sparse = p.idx != nullptr;

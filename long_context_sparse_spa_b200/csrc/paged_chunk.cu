@@ -54,7 +54,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kBase = 9.f, kSlack = 6.f;
 constexpr int kSpread = 11;               // powers of two over which scales in the same units are exact
-constexpr uint32_t kSpin = 1u << 22;
+constexpr uint32_t kSpin = 1u << 22, kStallSpin = 1u << 10;   // tries of a wait; with the test hook
 
 template <int D, bool INT4>
 struct ChunkShared {
@@ -67,6 +67,7 @@ struct ChunkShared {
     uint8_t raw[3][INT4 ? kHalf * ROWB : 16];
     uint64_t raw_full[3], raw_empty[3];
     uint32_t raw_valid[3][2];                          // tokens of the step that exist
+    uint32_t raw_end;                                  // steps copied before a wait of the copying warp gave up
     uint64_t s_full[2], p_full[2][2], pv_half[2];      // by row tile (and half of the tokens)
     uint64_t k_full[2], v_full[2], k_empty[2], v_empty[2], o_done, q_full;
     alignas(16) uint32_t pw[4][4];                     // the powers of two of tile t (slot t % 4) by 32 tokens: power_word
@@ -261,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
         mbar_init(&sh.o_done, 2);
         mbar_init(&sh.q_full, 256);
         sh.fail = 0;
+        sh.raw_end = 0xffffffffu;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     pdl_enter();
@@ -328,8 +330,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
     // bounded wait on a barrier's phase; on expiry, or once another thread's has expired, false
     auto wait = [&](uint64_t* bar, uint32_t par) -> bool {
         for (uint32_t it = 0; !mbar_try_wait(bar, par); ++it) {
-            if (it >= kSpin || ((it & 255u) == 255u && *reinterpret_cast<volatile int*>(&sh.fail))) {
-                if (it >= kSpin) raise_status(p.status, SPA_ERR_TIMEOUT);
+            if (it >= p.spin || ((it & 255u) == 255u && *reinterpret_cast<volatile int*>(&sh.fail))) {
+                if (it >= p.spin) raise_status(p.status, SPA_ERR_TIMEOUT);
                 *reinterpret_cast<volatile int*>(&sh.fail) = 1;
                 return false;
             }
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             auto all = [&](bool v) { return __all_sync(0xffffffffu, v) != 0; };
             // (a warp without a row tile waits for the queries all the same: it must not run ahead of a phase)
             bool live = all(wait(&sh.q_full, segs & 1)) && part && all(wait(&sh.k_full[base & 1], (base >> 1) & 1));
-            if (live) {
+            if (live && !p.stall) {
                 tc_fence_after();
                 s_mma(base);
                 commit(&sh.k_empty[base & 1]);
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 return h < steps && lane < runs && n < lim ? __ldg(pt + (n >> p.kv.page_shift)) : -1;
             };
             int pid = page_of(0);
-            for (int h = 0; h < steps; ++h) {
+            for (int h = 0; h < steps && sh.raw_end == 0xffffffffu; ++h) {
                 const uint32_t S = base_raw + uint32_t(h), slot = S % 3;
                 const int n = a * kKeys + h * kHalf + lane * R;
                 int rows = lane < runs ? min(max(lim - n, 0), R) : 0;
@@ -716,7 +718,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
                 if (rows > 0 && off < 0) raise_status(p.status, SPA_ERR_INVALID_ARG);
                 if (off < 0) rows = 0;
                 pid = page_of(h + 1);
-                if (S >= 3 && !__all_sync(0xffffffffu, wait(&sh.raw_empty[slot], (S / 3 - 1) & 1))) break;
+                if (S >= 3 && !__all_sync(0xffffffffu, wait(&sh.raw_empty[slot], (S / 3 - 1) & 1))) {
+                    if (lane == 0) sh.raw_end = S;     // nothing is copied any more, in later segments either
+                    break;
+                }
                 const uint32_t dst = smem_u32(sh.raw[slot]) + lane * R * ROWB;
                 uint32_t m0 = 0, m1 = 0;               // this lane's tokens among the step's 64
                 if (rows > 0) {
@@ -1157,6 +1162,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
     }
     tc_fence_before();
     __syncthreads();
+    if (sh.fail) {                                     // a wait gave up: what is in flight ends first, or has as long to
+        auto drain = [&](uint64_t* bar, uint32_t par) {
+            for (uint32_t it = 0; it < kSpin && !mbar_try_wait(bar, par); ++it) {
+            }
+        };
+        if (warp == 8 + kUnpack && segs) drain(&sh.o_done, (segs - 1) & 1);
+        if (INT4 && warp == 8 + kUnpack + 2) {
+            const uint32_t n = min(sh.raw_end, raw_done);
+            for (uint32_t S = n > 3 ? n - 3 : 0; S < n; ++S) drain(&sh.raw_full[S % 3], (S / 3) & 1);
+        }
+        __syncthreads();
+    }
     if (warp == 0) tmem_dealloc(tmem, 512);
 }
 
@@ -1171,7 +1188,10 @@ void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch) {
     p.partials = reinterpret_cast<float*>(scratch + align_up(size_t(device_info().num_sms) * 4, 256));
 }
 
-spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st) {
+spa_status launch_paged_chunk(const PagedAttendParams& args, cudaStream_t st) {
+    PagedAttendParams p = args;
+    p.stall = (test_stall_bits() & SPA_TEST_STALL_PAGED_CHUNK) != 0;
+    p.spin = p.stall ? kStallSpin : kSpin;
     const int sms = device_info().num_sms;
     const int TQ = paged_tokens_per_tile(256, p.Hq / p.kv.Hkv);
     // the prefix of a launch's sequences lies in shared memory, in 32 bits: a sequence's query tiles times its

@@ -114,3 +114,47 @@ def test_prefill_mma_timeout_is_reported_and_the_context_recovers():
         _, ref = oracle.prefill_block(cfg, x, j, g)
         rows, heads = slice(j * bq, (j + 1) * bq), slice(g * G, (g + 1) * G)
         check_outputs(out[rows, heads], out32[rows, heads], ref, f"recovered unit {(j, g)}")
+
+
+def _paged(new, fmt, d=128, lens=(3000, 40, 700, 17, 2000, 333)):
+    """A plan over random 4-bit or bf16 rows: sequences of several lengths, so that CTAs take several units and units are
+    split over CTAs."""
+    B, Hkv, page = len(lens), 2, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    width = -(-max(lens) // page)
+    pool = spa.paged_cache(B * width, Hkv, page, d, fmt)
+    kw = dict(cache=pool, page_table=torch.arange(B * width, dtype=torch.int32, device="cuda").reshape(B, width),
+              kv_len=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    rows = torch.randn(2, sum(lens), Hkv, d, generator=g, device="cuda").to(torch.bfloat16)
+    start = torch.tensor(np.concatenate(([0], np.cumsum(lens))), dtype=torch.int32, device="cuda")
+    spa.paged_append(k=rows[0], v=rows[1], seq_start=start, **kw)
+    q = torch.randn(B * new, 4 * Hkv, d, generator=g, device="cuda").to(torch.bfloat16)
+    return spa.paged_attend(q=q, sm_scale=d**-0.5, run=False, **kw,
+                            seq_start=torch.arange(0, B * new + 1, new, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("fmt", [spa.SPA_KV_INT4, spa.SPA_KV_BF16])
+@pytest.mark.parametrize("bit,new", [(_abi.SPA_TEST_STALL_PAGED_COPY, 1), (_abi.SPA_TEST_STALL_PAGED_COPY, 5),
+                                     (_abi.SPA_TEST_STALL_PAGED_CHUNK, 17)])
+def test_paged_attention_timeouts_are_reported_and_the_workspace_recovers(bit, new, fmt):
+    plan = _paged(new, fmt)
+    plan.run()
+    torch.cuda.synchronize()
+    assert spa.read_device_status(plan.ws) == 0
+    out, lse = plan.out.clone(), plan.lse.clone()
+    assert torch.isfinite(lse).all()
+    for _ in range(2):
+        with stalled(bit):
+            plan.run()
+            torch.cuda.synchronize()
+        assert spa.read_device_status(plan.ws) & TIMEOUT
+        plan.out.fill_(9)
+        plan.run()                      # the same workspace, hook off
+        torch.cuda.synchronize()
+        assert spa.read_device_status(plan.ws) == 0
+        assert torch.equal(plan.out, out) and torch.equal(plan.lse, lse)
+    other = _abi.SPA_TEST_STALL_PAGED_COPY + _abi.SPA_TEST_STALL_PAGED_CHUNK - bit
+    with stalled(other):                # the other kernel's bit means nothing to this one
+        plan.run()
+        torch.cuda.synchronize()
+    assert spa.read_device_status(plan.ws) == 0 and torch.equal(plan.out, out)

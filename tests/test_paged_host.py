@@ -229,3 +229,10 @@ def test_python_refuses_cpu_tensors_and_wrong_types():
         spa.paged_gather(cache=c.float(), page_table=t, kv_len=n, N=4)
     with pytest.raises(ValueError):
         spa.paged_cache(4, 2, 16, 128, fmt=9)
+
+
+def test_the_paged_kernels_have_their_bits_of_the_stall_hook():
+    L = _abi.lib()
+    bits = _abi.SPA_TEST_STALL_PAGED_COPY | _abi.SPA_TEST_STALL_PAGED_CHUNK
+    assert L.spa_test_stall(bits) == _abi.SPA_OK and L.spa_test_stall(bits | 32) == _abi.SPA_ERR_INVALID_ARG
+    assert L.spa_test_stall(0) == _abi.SPA_OK
