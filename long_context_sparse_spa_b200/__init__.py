@@ -654,7 +654,9 @@ def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
     """Exact softmax attention of the new tokens over a paged cache (bf16 or 4-bit); see spa_paged_attend in
     include/spa.h.  q [T, Hq, d] bf16.  Whole cache: every query sees the tokens up to its own; seq_start
     [B + 1] int32 groups several queries per sequence.  Supports: idx [U, cap], count [U] int32 as select_topk
-    and select_topp give them, at most one query per sequence.  plan.out [T, Hq, d] bf16, plan.out_f32, plan.lse [T, Hq]."""
+    and select_topp give them, at most one query per sequence.  plan.out [T, Hq, d] bf16, plan.out_f32, plan.lse [T, Hq].
+    ws: the workspace of an earlier plan, if it is large enough, for plans that do not run at the same time (plans of
+    different T among them, as a serving loop builds them); they share its status word."""
     kv = _paged_kv(cache, page_table, kv_len)
     _rows(q, "q", None, kv.d)
     T, Hq, d = q.shape

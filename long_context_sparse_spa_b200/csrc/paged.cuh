@@ -41,7 +41,7 @@ struct PagedAttendParams {
     uint16_t* out;              // [T, Hq, d]
     float* out_f32;
     float* lse;                 // [T, Hq]
-    int* arrived;               // [CTAs]: finished shares of the split unit that starts in a CTA; 0 between calls
+    int* arrived;               // [2 * SMs]: finished shares of the split unit that starts in a CTA; 0 between calls
     float* partials;            // [2 * CTAs] shares of split units
     uint32_t* status;
     uint32_t spin;              // tries of a bounded wait
@@ -49,7 +49,6 @@ struct PagedAttendParams {
 };
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse);
-void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch);   // the workspace after its header
 // paged_chunk.cu: more than 32 rows per sequence and kv head on average.  16 sequences of 4096, 32 / 8 heads, mma.sync
 // and tcgen05: 4-bit 72 and 110 us at 32 rows; bf16 91 and 107 us at 32 rows, 156 and 105 us at 36.
 inline bool paged_chunk_taken(const void* seq_start, const void* idx, int T, int Hq, int Hkv, int B,
@@ -58,7 +57,14 @@ inline bool paged_chunk_taken(const void* seq_start, const void* idx, int T, int
 }
 spa_status launch_paged_chunk(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_chunk_scratch_bytes(int d);
-void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch);
+// The workspace after its header: arrival counters, 0 between calls, then the shares of split units, of no meaning
+// between calls.  Both kernels have their counters in the same place, so that a workspace that is large enough serves
+// calls of either in turn.
+inline size_t paged_counter_bytes() { return align_up(size_t(device_info().num_sms) * 2 * sizeof(int), 256); }
+inline void paged_carve(PagedAttendParams& p, uint8_t* scratch) {
+    p.arrived = reinterpret_cast<int*>(scratch);
+    p.partials = reinterpret_cast<float*>(scratch + paged_counter_bytes());
+}
 constexpr int kPagedMaxUnits = 512;   // sequences, or supports, of one launch: 4 bytes of shared memory each
 
 }  // namespace spa

@@ -168,11 +168,8 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     p.out_f32 = a->out_f32;
     p.lse = a->lse;
     p.status = reinterpret_cast<uint32_t*>(w);
-    if (chunk_taken(a)) {
-        paged_chunk_carve(p, w + kWsHeader);
-        return launch_paged_chunk(p, static_cast<cudaStream_t>(stream));
-    }
-    paged_attend_carve(p, w + kWsHeader);
+    paged_carve(p, w + kWsHeader);
+    if (chunk_taken(a)) return launch_paged_chunk(p, static_cast<cudaStream_t>(stream));
     return launch_paged_attend(p, static_cast<cudaStream_t>(stream));
 }
 

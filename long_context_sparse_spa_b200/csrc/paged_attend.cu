@@ -1124,18 +1124,13 @@ static void paged_shape(int T, int B, int heads, bool sparse, int* nt, int* TQ) 
     *nt = (rows + 7) / 8;
     *TQ = sparse || T <= B ? 1 : paged_tokens_per_tile(*nt * 8, heads);
 }
-static size_t paged_attend_grid_max() { return size_t(device_info().num_sms) * 2; }
 
-// Workspace after the header: [2 * SMs] arrival counters, then two shares for each CTA.
+// two shares for each of up to two CTAs per SM
 size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse) {
-    const size_t grid = paged_attend_grid_max();
+    const size_t grid = size_t(device_info().num_sms) * 2;
     int nt, TQ;
     paged_shape(T, B, heads, sparse, &nt, &TQ);
-    return align_up(grid * 4, 256) + align_up(2 * grid * paged_rec_floats(d, nt * 8) * 4, 256);
-}
-void paged_attend_carve(PagedAttendParams& p, uint8_t* scratch) {
-    p.arrived = reinterpret_cast<int*>(scratch);
-    p.partials = reinterpret_cast<float*>(scratch + align_up(paged_attend_grid_max() * 4, 256));
+    return paged_counter_bytes() + align_up(2 * grid * paged_rec_floats(d, nt * 8) * 4, 256);
 }
 
 spa_status launch_paged_attend(const PagedAttendParams& args, cudaStream_t st) {

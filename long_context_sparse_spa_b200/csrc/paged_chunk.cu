@@ -1180,12 +1180,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
 }  // namespace
 
 size_t paged_chunk_scratch_bytes(int d) {
-    const size_t grid = device_info().num_sms;
-    return align_up(grid * 4, 256) + align_up(2 * grid * chunk_rec_floats(d) * 4, 256);
-}
-void paged_chunk_carve(PagedAttendParams& p, uint8_t* scratch) {
-    p.arrived = reinterpret_cast<int*>(scratch);
-    p.partials = reinterpret_cast<float*>(scratch + align_up(size_t(device_info().num_sms) * 4, 256));
+    const size_t grid = device_info().num_sms;         // two shares for each CTA
+    return paged_counter_bytes() + align_up(2 * grid * chunk_rec_floats(d) * 4, 256);
 }
 
 spa_status launch_paged_chunk(const PagedAttendParams& args, cudaStream_t st) {

@@ -1030,3 +1030,29 @@ def test_append_of_many_sequences():
         for i in range(new[b]):
             want[c.table[b, 0], :, i] = rows[start[b] + i]
     assert (_np(c.pool) == want).all()
+
+
+def test_one_workspace_serves_every_attention_call_in_turn():
+    # decode, drafted tokens, chunks of both formats and head sizes, supports: one after the other on one workspace, all of
+    # them with units that are split over CTAs
+    L = 40_000
+    plans = []
+    for fmt, d, new in [(INT4, 128, 1), (BF16, 64, 60), (INT4, 128, 5), (INT4, 128, 60), (BF16, 128, 1), (INT4, 64, 1)]:
+        c = Cache([L], 1, d, 64, fmt, seed=71, fill=False)
+        c.pool.random_(0, 255) if fmt == INT4 else c.pool.normal_()
+        if fmt == INT4:                     # any codes will do; scales of one
+            c.pool.view(torch.bfloat16)[..., d // 2:] = 1.0
+        q = torch.randn(new, 4, d, device="cuda").to(torch.bfloat16)
+        plans.append(dict(q=q, sm_scale=0.02, seq_start=_i32([0, new]), **c.kw))
+        if new == 1:
+            plans.append(dict(q=q, sm_scale=0.02, idx=torch.arange(0, L, 2, dtype=torch.int32, device="cuda")[None],
+                              count=_i32([L // 2]), **c.kw))
+    alone = [spa.paged_attend(**kw) for kw in plans]
+    ws = spa.workspace(max(p.ws.numel() for p in alone))
+    shared = [spa.paged_attend(ws=ws, run=False, **kw) for kw in plans]
+    for order in (range(len(plans)), reversed(range(len(plans))), [0, 3, 0, 4, 6, 1, 1, 2, 5]):
+        for i in order:
+            shared[i].out.fill_(9)
+            shared[i].run()
+            assert torch.equal(shared[i].out, alone[i].out) and torch.equal(shared[i].lse, alone[i].lse), i
+    assert spa.read_device_status(ws) == 0
