@@ -236,3 +236,17 @@ def test_the_paged_kernels_have_their_bits_of_the_stall_hook():
     bits = _abi.SPA_TEST_STALL_PAGED_COPY | _abi.SPA_TEST_STALL_PAGED_CHUNK
     assert L.spa_test_stall(bits) == _abi.SPA_OK and L.spa_test_stall(bits | 32) == _abi.SPA_ERR_INVALID_ARG
     assert L.spa_test_stall(0) == _abi.SPA_OK
+
+
+def test_every_header_of_the_sources_makes_the_library_stale():
+    import re
+
+    from long_context_sparse_spa_b200 import build
+
+    deps = {os.path.realpath(f) for f in build._deps()}
+    for src in sorted(deps):
+        with open(src) as f:
+            for name in re.findall(r'^#include "([^"]+)"', f.read(), re.M):
+                at = [os.path.join(d, name) for d in (os.path.dirname(src), build.CSRC, build.INCLUDE)]
+                found = [os.path.realpath(p) for p in at if os.path.exists(p)]
+                assert found and found[0] in deps, f"{os.path.basename(src)} includes {name}"
