@@ -675,7 +675,8 @@ def paged_attend(*, q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tens
         _need(count, torch.int32, "count")
         if idx.dim() != 2 or idx.shape[0] != U or tuple(count.shape) != (U,):
             raise ValueError(f"idx must be [{U}, cap] and count [{U}]")
-        a.idx, a.count, a.cap = _ptr(idx), _ptr(count), idx.shape[1]
+        # (a tensor without elements has no address: with cap = 0 nothing is read behind it)
+        a.idx, a.count, a.cap = _ptr(idx) or _ptr(count), _ptr(count), idx.shape[1]
     _same_device(cache, q=q, seq_start=seq_start, idx=idx, count=count)
     dev = cache.device
     out = torch.empty((T, Hq, d), dtype=torch.bfloat16, device=dev)

@@ -1056,3 +1056,15 @@ def test_one_workspace_serves_every_attention_call_in_turn():
             shared[i].run()
             assert torch.equal(shared[i].out, alone[i].out) and torch.equal(shared[i].lse, alone[i].lse), i
     assert spa.read_device_status(ws) == 0
+
+
+def test_supports_without_room_for_an_entry():
+    c = Cache([20, 0], 2, 64, 16, INT4, seed=72)
+    q = torch.randn(2, 4, 64, device="cuda").to(torch.bfloat16)
+    for count in (0, 3):                    # (a count above cap is cut)
+        plan = spa.paged_attend(q=q, sm_scale=0.1, idx=torch.empty((4, 0), dtype=torch.int32, device="cuda"),
+                                count=_i32([count] * 4), run=False, **c.kw)
+        plan.out.fill_(9)
+        plan.run()
+        assert spa.read_device_status(plan.ws) == 0
+        assert (plan.out == 0).all() and (plan.lse == -np.inf).all()
