@@ -592,7 +592,8 @@ typedef struct spa_paged_attend_args {
 } spa_paged_attend_args;
 
 spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_bytes, void* stream);
-/* Depends on the arguments other than the pointers' values and on the current device's SM count. */
+/* Depends on the arguments other than the pointers' values and on the current device's SM count; 0
+ * for arguments that have none. */
 size_t spa_paged_attend_workspace_bytes(const spa_paged_attend_args* a);
 
 /* ------------------------------------------------------------------------------------

@@ -125,7 +125,8 @@ static bool chunk_taken(const spa_paged_attend_args* a) {
 }
 
 size_t spa_paged_attend_workspace_bytes(const spa_paged_attend_args* a) {
-    if (!a || a->kv.d <= 0 || a->kv.Hkv <= 0 || a->kv.B <= 0 || a->T < 0 || a->Hq < 0) return 0;
+    if (!a || a->kv.d <= 0 || a->kv.Hkv <= 0 || a->kv.B <= 0 || a->T < 0) return 0;
+    if (a->Hq <= 0 || a->Hq % a->kv.Hkv) return 0;     // (no heads per kv head to divide by)
     if (chunk_taken(a)) return kWsHeader + paged_chunk_scratch_bytes(a->kv.d);
     const bool sparse = a->idx != nullptr;
     const int heads = sparse && a->collapse == SPA_COLLAPSE_NONE ? 1 : a->Hq / a->kv.Hkv;

@@ -250,3 +250,11 @@ def test_every_header_of_the_sources_makes_the_library_stale():
                 at = [os.path.join(d, name) for d in (os.path.dirname(src), build.CSRC, build.INCLUDE)]
                 found = [os.path.realpath(p) for p in at if os.path.exists(p)]
                 assert found and found[0] in deps, f"{os.path.basename(src)} includes {name}"
+
+
+def test_heads_that_do_not_divide():
+    L = _abi.lib()
+    for hq in (0, -2, 1, 3):                # kv heads: 2
+        t = _abi.SpaPagedAttendArgs(kv=_kv(), T=5, Hq=hq, q=256, out=256, seq_start=256, sm_scale=1.0)
+        assert L.spa_paged_attend_workspace_bytes(ctypes.byref(t)) == 0
+        assert _call("spa_paged_attend", t) == "SPA_ERR_INVALID_ARG"
