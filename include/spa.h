@@ -574,7 +574,7 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
  * its token's four are off by up to 2^-19 of that largest, and all by up to 2^-89 (keys too in
  * calls with more than 32 rows, a query of a head each, per sequence and kv head on average).
  * What a query does not see does not reach it, values that are not finite included.
- * Hq / Hkv <= 16; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(a); a workspace serves, one
+ * Hq / Hkv <= 16, Hq < 65536; |q| < 2^113.  ws >= spa_paged_attend_workspace_bytes(a); a workspace serves, one
  * after the other, whatever calls it is large enough for. */
 typedef struct spa_paged_attend_args {
     spa_paged_kv kv;

@@ -145,7 +145,8 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
     if (!a->out || !ws || (a->idx == nullptr) != (a->count == nullptr)) return SPA_ERR_INVALID_ARG;
     s = check_rows(a->q, a->q_token_stride, a->q_head_stride);
     if (s != SPA_OK) return s;
-    if (a->Hq / a->kv.Hkv > 16) return SPA_ERR_UNSUPPORTED_SHAPE;
+    // (channels of a query tile's rows, 256 tokens of all heads, are counted in 32 bits)
+    if (a->Hq / a->kv.Hkv > 16 || a->Hq > 65535) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (!aligned16(a->out) || !aligned16(a->out_f32) || !aligned16(ws)) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (a->idx) {
         if (a->T > a->kv.B || a->cap < 0 || a->unit_tokens <= 0) return SPA_ERR_INVALID_ARG;

@@ -258,3 +258,9 @@ def test_heads_that_do_not_divide():
         t = _abi.SpaPagedAttendArgs(kv=_kv(), T=5, Hq=hq, q=256, out=256, seq_start=256, sm_scale=1.0)
         assert L.spa_paged_attend_workspace_bytes(ctypes.byref(t)) == 0
         assert _call("spa_paged_attend", t) == "SPA_ERR_INVALID_ARG"
+
+
+def test_heads_that_are_too_many():
+    for hq, hkv in ((65536, 4096), (65536, 32768), (1 << 20, 65536)):
+        t = _abi.SpaPagedAttendArgs(kv=_kv(Hkv=hkv), T=2, Hq=hq, q=256, out=256)
+        assert _call("spa_paged_attend", t) == "SPA_ERR_UNSUPPORTED_SHAPE"
