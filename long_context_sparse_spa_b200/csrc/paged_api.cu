@@ -35,7 +35,7 @@ spa_status check_kv(const spa_paged_kv& kv, bool* noop, PagedView* v) {
     v->page_shift = shift;
     v->d = kv.d;
     v->B = kv.B;
-    v->max_pages = kv.max_pages;
+    v->max_pages = kv.num_pages > 0 ? kv.max_pages : 0;   // without a page nothing is looked up: a length above 0 is an error
     v->int4 = kv.format == SPA_KV_INT4;
     v->row_bytes = paged_row_bytes(v->int4, kv.d);
     return SPA_OK;

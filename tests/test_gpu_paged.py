@@ -1068,3 +1068,20 @@ def test_supports_without_room_for_an_entry():
         plan.run()
         assert spa.read_device_status(plan.ws) == 0
         assert (plan.out == 0).all() and (plan.lse == -np.inf).all()
+
+
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+@pytest.mark.parametrize("new", [1, 5, 60])
+def test_a_pool_without_pages(fmt, new):
+    pool = spa.paged_cache(0, 1, 16, 128, fmt)
+    kw = dict(cache=pool, page_table=_i32([[0] * 9, [0] * 9]), kv_len=_i32([130, 0]))
+    q = torch.randn(new, 4, 128, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32([0, new, new]), run=False, **kw)
+    plan.out.fill_(9)
+    plan.run()
+    assert spa.read_device_status(plan.ws) == INVALID
+    assert (plan.out == 0).all() and (plan.lse == -np.inf).all()
+    add = spa.paged_append(k=q[:, :1], v=q[:, 1:2], seq_start=_i32([0, new, new]), **kw)
+    assert spa.read_device_status(add.ws) == INVALID
+    got = spa.paged_gather(N=40, **kw)
+    assert spa.read_device_status(got.ws) == INVALID and (got.K == 0).all()
