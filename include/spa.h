@@ -527,8 +527,9 @@ size_t spa_paged_row_bytes(int format, int d);   /* 0 for an unknown format */
  *   4-bit rows: the scale is amax / 7 of the group rounded up to bf16, the code the nearest
  *   (even) integer to x / scale plus 8, from the keys as rotated (not rounded to bf16 first), so
  *   |x - value| <= scale / 2 up to binary32 rounding.
- * Two tokens of one call that name the same slot leave either of them.  rot a multiple of 16,
- * 0 .. d (0: no rotation, inv_freq unused).  ws NULL (no status word) or >= 256 bytes. */
+ * Two tokens of one call must not name the same slot: its row would be a mixture of theirs, codes
+ * of one beside scales of the other.  rot a multiple of 16, 0 .. d (0: no rotation, inv_freq
+ * unused).  ws NULL (no status word) or >= 256 bytes. */
 typedef struct spa_paged_append_args {
     spa_paged_kv kv;
     int T, Hq;

@@ -1085,3 +1085,23 @@ def test_a_pool_without_pages(fmt, new):
     assert spa.read_device_status(add.ws) == INVALID
     got = spa.paged_gather(N=40, **kw)
     assert spa.read_device_status(got.ws) == INVALID and (got.K == 0).all()
+
+
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+def test_two_tokens_of_one_slot_leave_a_mixture_of_theirs(fmt):
+    # sequences that share a page, against the rules: nothing else is written, and every piece is of one of the two
+    d = 128
+    c = Cache([3, 3], 2, d, 16, fmt, fill=False)
+    c.kw["page_table"][1] = c.kw["page_table"][0]
+    c.pool.view(torch.uint8).fill_(0xA5)
+    kv = torch.randn(2, 2, 2, d, device="cuda").to(torch.bfloat16)
+    add = spa.paged_append(k=kv[0], v=kv[1], **c.kw)
+    assert spa.read_device_status(add.ws) == 0
+    host = _np(c.pool.view(torch.uint8)).reshape(c.pool.shape[0], 2, 16, -1)
+    k, v = _bf(kv[0]).astype(np.float32), _bf(kv[1]).astype(np.float32)
+    rows = ref.pack(k, v) if fmt == INT4 else np.concatenate((ref.bf16_bits(k), ref.bf16_bits(v)), -1).astype("<u2").view(np.uint8)
+    got = host[c.table[0, 0], :, 2].copy().view("<u2")
+    a, b = rows[0].copy().view("<u2"), rows[1].copy().view("<u2")
+    assert ((got == a) | (got == b)).all()
+    host[c.table[0, 0], :, 2] = 0xA5
+    assert (host == 0xA5).all()
