@@ -11,7 +11,9 @@ Tolerances, derived before any run.  Of token j with logit x, weight p (binary64
   by half a step of its type besides: 2^-11 (4-bit rows, fp16), 2^-16 (bf16 rows, two bf16 parts);
 - out is off by sum p (eps + step) |v| + |out| sum p eps, and by n 2^-23 sum p |v| for the binary32 accumulation;
 - fp16 has an absolute floor, multiples of 2^-24: weights times a token's value scale are held in units in which the
-  largest is at least 2^9, each off by at most 2^-34 of that largest, a code is at most 8: n 2^-31 of it over n tokens.
+  largest is at least 2^9, each off by at most 2^-34 of that largest, a code is at most 8: n 2^-31 of it over n tokens;
+- a 4-bit value, and a key in calls of more than 32 rows, is a multiple of 2^-24 in units in which its token's largest
+  scale is 2^-6 or more: exact where its own scale is at least 2^-11 of that largest, else off by 2^-19 of it ("apart").
 Everything is checked on out_f32, before the last rounding.
 """
 import numpy as np
@@ -46,7 +48,7 @@ def put(c, b, n, k, v):
     c.K[b][:, n], c.V[b][:, n] = K[:, 0], V[:, 0]
 
 
-def check_closely(c, q, out, lse, sees, sm_scale, b, what):
+def check_closely(c, q, out, lse, sees, sm_scale, b, what, apart=False, floor=1e-40):
     """q [G, d], out [G, d] fp32 of one token and the one kv head, sees [n] bool."""
     K, V = c.K[b][0][sees], c.V[b][0][sees]
     n = len(K)
@@ -57,13 +59,17 @@ def check_closely(c, q, out, lse, sees, sm_scale, b, what):
         p = np.exp(x - z)
         per = np.repeat(c.ks[b][0][sees], c.d // 4, -1) * 15 if c.fmt == INT4 else np.abs(K)
         delta = sm_scale * (per * np.abs(q[h])).sum(-1) * 128 * 2.0**-23
+        if apart:
+            delta = delta + sm_scale * 2.0**-19 * c.ks[b][0][sees].max(-1) * np.abs(q[h]).sum()
         eps = 2 * delta + 2.0**-22 * (np.abs(x) + abs(z) + 130) + 2.0**-20
         off = (p * eps).sum()
         step = 2.0**-11 if c.fmt == INT4 else 2.0**-16
         tol = (p * (eps + step)) @ np.abs(V) + np.abs(o) * off + n * 2.0**-23 * (p @ np.abs(V))
         if c.fmt == INT4:
             tol = tol + n * 2.0**-31 * (p * c.vs[b][0][sees].max(-1)).max()
-        tol = tol * 1.01 + 1e-40
+        if apart:
+            tol = tol + 2.0**-19 * (p * c.vs[b][0][sees].max(-1)).sum()
+        tol = tol * 1.01 + floor
         err = np.abs(out[h] - o)
         assert (err <= tol).all(), f"{what}, head {h}: out off by {(err / tol).max():.2f} of the tolerance"
         assert abs(lse[h] - z) <= off + 2.0**-21 * max(abs(z), 200), f"{what}, head {h}: lse {lse[h]} vs {z}"
@@ -112,3 +118,35 @@ def test_values_of_equal_tokens_come_back_exactly(d, L, new):
         v = c.V[t // new][0, 0]
         err = np.abs(out[t] - v)
         assert (err <= np.abs(v) * (2.0**-18 + L * 2.0**-23)).all(), f"row {t}: off by {(err / np.abs(v).max()).max():.2e}"
+
+
+@pytest.mark.parametrize("fmt", [INT4, BF16])
+@pytest.mark.parametrize("new", [60, 5, 1])
+@pytest.mark.parametrize("vs", [1e-22, 1e-30])
+def test_tiny_values(fmt, new, vs):
+    # bf16 rows: whatever the size.  4-bit rows: exact down to scales of 2^-81, below within 2^-89
+    c = Cache([400], 1, 128, 16, fmt, seed=63, vscale=vs)
+    q = torch.randn(new, 4, 128, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.09, seq_start=_i32([0, new]), want_f32=True, **c.kw)
+    for i in sorted({0, new // 2, new - 1}):
+        check_closely(c, _bf(q)[i], _np(plan.out_f32)[i].astype(np.float64), _np(plan.lse)[i].astype(np.float64),
+                      np.arange(400) <= 400 - new + i, 0.09, 0, f"query {i}",
+                      floor=2.0**-89 if fmt == INT4 and vs < 1e-24 else 1e-40)
+
+
+@pytest.mark.parametrize("d", [128, 64])
+@pytest.mark.parametrize("new", [60, 5, 1])
+@pytest.mark.parametrize("span", [9, 20])
+def test_groups_of_a_token_that_lie_far_apart(d, new, span):
+    c = Cache([400], 1, d, 16, INT4, seed=64)
+    rng = np.random.default_rng(64)
+    for n in range(400):
+        far = 2.0 ** -rng.integers(0, span + 1, (2, 4))
+        far[:, rng.integers(0, 4)] = 1
+        k, v = rng.standard_normal((2, d)) * np.repeat(far, d // 4, -1)
+        put(c, 0, n, k, v)
+    q = torch.randn(new, 4, d, device="cuda").to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=0.1, seq_start=_i32([0, new]), want_f32=True, **c.kw)
+    for i in sorted({0, new // 2, new - 1}):
+        check_closely(c, _bf(q)[i], _np(plan.out_f32)[i].astype(np.float64), _np(plan.lse)[i].astype(np.float64),
+                      np.arange(400) <= 400 - new + i, 0.1, 0, f"query {i}", apart=span > 9)
