@@ -523,7 +523,8 @@ size_t spa_paged_row_bytes(int format, int d);   /* 0 for an unknown format */
  *   binary64, the rotation in binary32.
  *   k, v   [T, Hkv, d] bf16 with the given token and head strides (elements, multiples of 8;
  *          slices of a fused projection need no copy); 16-byte aligned
- *   q      [T, Hq, d] likewise, or NULL; q_out [T, Hq, d] bf16 dense, must not overlap q, k or v
+ *   q      [T, Hq, d] likewise, or NULL; q_out [T, Hq, d] bf16 dense, which must not lie in the
+ *          stretch of q, k or v from first to last element (refused)
  *   4-bit rows: the scale is amax / 7 of the group rounded up to bf16, the code the nearest
  *   (even) integer to x / scale plus 8, from the keys as rotated (not rounded to bf16 first), so
  *   |x - value| <= scale / 2 up to binary32 rounding.
@@ -568,7 +569,7 @@ spa_status spa_paged_gather(const spa_paged_gather_args* a, void* ws, size_t ws_
  *   (e + 1) * unit_tokens) below kv_len[b]; U = B * Hkv (collapse GROUP_MEAN) or B * Hq (NONE).
  *   q [T, Hq, d] bf16 with token and head strides (elements, multiples of 8), 16-byte aligned;
  *   out [T, Hq, d] bf16, out_f32 [T, Hq, d] fp32 (optional), both 16-byte aligned as ws is;
- *   lse [T, Hq] fp32 (optional).
+ *   lse [T, Hq] fp32 (optional).  out and out_f32 must not lie in q's stretch (refused).
  * A query that sees nothing gives out = 0 and lse = -inf.  Weights are carried in 11 bits (4-bit
  * cache: fp16) or about 16 (bf16 cache), sums in binary32.  4-bit values enter as they are (scale *
  * (code - 8), exactly), except that those of a group whose scale is below 2^-11 of the largest of

@@ -49,6 +49,13 @@ spa_status check_rows(const void* p, int64_t tok, int64_t head) {
     return SPA_OK;
 }
 
+// whether out [T, Hq, d] of `bytes` per element reaches into the stretch of rows [T, heads, d] at p
+bool overlaps(const void* out, size_t bytes, int T, int Hq, int d, const uint16_t* p, int heads, int64_t tok, int64_t head) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), r = reinterpret_cast<uintptr_t>(p);
+    const uintptr_t o1 = o + uintptr_t(T) * Hq * d * bytes, r1 = r + 2 * (uintptr_t(T - 1) * tok + uintptr_t(heads - 1) * head + d);
+    return o < r1 && r < o1;
+}
+
 }  // namespace
 }  // namespace spa
 
@@ -76,6 +83,11 @@ spa_status spa_paged_append(const spa_paged_append_args* a, void* ws, size_t ws_
     if (s != SPA_OK) return s;
     if (a->q && (!a->q_out || a->q_out == a->q)) return SPA_ERR_INVALID_ARG;
     if (a->q && !aligned16(a->q_out)) return SPA_ERR_UNSUPPORTED_SHAPE;
+    const int d = a->kv.d, Hkv = a->kv.Hkv;
+    if (a->q && (overlaps(a->q_out, 2, a->T, a->Hq, d, a->q, a->Hq, a->q_token_stride, a->q_head_stride) ||
+                 overlaps(a->q_out, 2, a->T, a->Hq, d, a->k, Hkv, a->k_token_stride, a->k_head_stride) ||
+                 overlaps(a->q_out, 2, a->T, a->Hq, d, a->v, Hkv, a->v_token_stride, a->v_head_stride)))
+        return SPA_ERR_INVALID_ARG;
     if (a->rot < 0 || a->rot > a->kv.d || (a->rot > 0 && !a->inv_freq)) return SPA_ERR_INVALID_ARG;
     if (a->rot % 16) return SPA_ERR_UNSUPPORTED_SHAPE;
     if (ws && ws_bytes < kWsHeader) return SPA_ERR_WORKSPACE_TOO_SMALL;
@@ -153,6 +165,9 @@ spa_status spa_paged_attend(const spa_paged_attend_args* a, void* ws, size_t ws_
         if (a->collapse != SPA_COLLAPSE_NONE && a->collapse != SPA_COLLAPSE_GROUP_MEAN) return SPA_ERR_INVALID_ARG;
     }
     if (ws_bytes < spa_paged_attend_workspace_bytes(a)) return SPA_ERR_WORKSPACE_TOO_SMALL;
+    if (overlaps(a->out, 2, a->T, a->Hq, a->kv.d, a->q, a->Hq, a->q_token_stride, a->q_head_stride) ||
+        (a->out_f32 && overlaps(a->out_f32, 4, a->T, a->Hq, a->kv.d, a->q, a->Hq, a->q_token_stride, a->q_head_stride)))
+        return SPA_ERR_INVALID_ARG;
     uint8_t* const w = static_cast<uint8_t*>(ws);
     p.T = a->T;
     p.Hq = a->Hq;

@@ -264,3 +264,16 @@ def test_heads_that_are_too_many():
     for hq, hkv in ((65536, 4096), (65536, 32768), (1 << 20, 65536)):
         t = _abi.SpaPagedAttendArgs(kv=_kv(Hkv=hkv), T=2, Hq=hq, q=256, out=256)
         assert _call("spa_paged_attend", t) == "SPA_ERR_UNSUPPORTED_SHAPE"
+
+
+def test_outputs_over_inputs_are_refused():
+    # T = 2 tokens of (4 + 2 + 2) heads of 128 in one projection: 4096 bytes of it, q at 1 << 20, k and v behind it
+    at = 1 << 20
+    for q_out in (at + 16, at + 4096 - 16, at - 16, at + 1024, at + 1536, at + 2048 + 1536):
+        a = _abi.SpaPagedAppendArgs(kv=_kv(), T=2, Hq=4, q=at, k=at + 1024, v=at + 1536, q_out=q_out, q_token_stride=1024,
+                                    k_token_stride=1024, v_token_stride=1024, q_head_stride=128, k_head_stride=128,
+                                    v_head_stride=128)
+        assert _call("spa_paged_append", a) == "SPA_ERR_INVALID_ARG", q_out - at
+    for kw in (dict(out=at + 1024), dict(out=at - 2032), dict(out_f32=at - 4080), dict(out=at + 2048 + 1008)):
+        t = _abi.SpaPagedAttendArgs(kv=_kv(), **{**dict(T=2, Hq=4, q=at, out=1 << 24, q_token_stride=1024, q_head_stride=128), **kw})
+        assert _call("spa_paged_attend", t) == "SPA_ERR_INVALID_ARG", kw
