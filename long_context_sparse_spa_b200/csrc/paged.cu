@@ -16,9 +16,11 @@
 // Each row of d channels is held by d/8 lanes, 8 channels (16 bytes) each; pair partners and group
 // maxima are exchanged by shuffles, so a row is read once.
 //
-// Measured on B200: append of 4096 tokens (32 query, 8 kv heads, d = 128) in 4 bits about 33 us and 8 us for reading
-// them back, 88 + 22 MB; bound by instruction issue (rotation and quantisation of 16-byte pieces).  Gather of 28672
-// 4-bit tokens of 8 heads to bf16 (150 MB) 28.7 us, 5.2 TB/s, bound by memory and shared memory together.
+// Measured on B200: append of 4096 tokens (32 query, 8 kv heads, d = 128) in 4 bits about 34 us and 8 us for reading
+// them back, 88 + 22 MB; the append uses 75 % of the issue slots (rotation and quantisation of 16-byte pieces).  Gather
+// of 28672 4-bit tokens of 8 heads to bf16 (150 MB) 29.4 us, 5.1 TB/s: its warps wait for shared memory, through which
+// the rows go in and out, twice as long as for DRAM.  Gather of 42 MB of bf16 rows 11.1 us, 3.8 TB/s (6.8 us where they
+// lie in L2): it waits for its loads, four of 16 bytes to a lane.
 #include <climits>
 
 #include "paged.cuh"

@@ -50,7 +50,9 @@ struct PagedAttendParams {
 spa_status launch_paged_attend(const PagedAttendParams& p, cudaStream_t st);
 size_t paged_attend_scratch_bytes(int d, int T, int B, int heads, bool sparse);
 // paged_chunk.cu: more than 32 rows per sequence and kv head on average.  16 sequences of 4096, 32 / 8 heads, mma.sync
-// and tcgen05: 4-bit 72 and 110 us at 32 rows; bf16 91 and 107 us at 32 rows, 156 and 105 us at 36.
+// and tcgen05: 4-bit 72 and 95 us at 32 rows, 118 and 95 at 36; bf16 95 and 106 us at 32 rows, 165 and 107 at 36.
+// All rows of a call go the same way: 64 sequences of 4096 with one token and one with 1024 take 512 us in one call, in
+// two calls 91 and 122; measured with equal sequences only, the rule is wrong for such a batch.
 inline bool paged_chunk_taken(const void* seq_start, const void* idx, int T, int Hq, int Hkv, int B,
                               float sm_scale) {
     return seq_start && !idx && sm_scale > 0.f && (long long)T * (Hq / Hkv) > 32ll * B;

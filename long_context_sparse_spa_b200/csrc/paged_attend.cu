@@ -4,7 +4,7 @@
 // Work split: a unit is one tile of up to 32 (query, head) rows that share the keys of one (sequence,
 // kv head), or one support.  Its keys are cut into tiles of TILE tokens; the tiles of all units form one
 // list (each unit charged kSeg tiles for its start-up and merge), split evenly over the CTAs (one per
-// SM).  Inside a CTA the warps take a unit's tiles round-robin; each warp copies its tiles into its own
+// SM; two for 4-bit rows and up to eight rows of a unit).  Inside a CTA the warps take a unit's tiles round-robin; each warp copies its tiles into its own
 // ring with bulk asynchronous copies, one per run of tokens that lie together on a page.
 //
 // Math per 16 tokens on tensor cores (mma.sync m16n8k16, fp32 accumulation), transposed so that tokens
@@ -29,10 +29,11 @@
 // partial (o, m, l) if the unit is split; the last CTA of a split unit to finish merges its partials in the
 // order of the CTAs, so equal calls give equal bits.
 //
-// Measured on B200: 4-bit, 4 sequences of 128K, 32 query / 4 kv heads, d = 128 (302 MB): 81 us, 3.7 TB/s; bound by
-// instruction issue (about 630 per 32 tokens and 8 heads beside the start and the merge; copying alone takes 66 us
-// with them).  bf16, 64K: 90 us, 5.9 TB/s; bound by memory.  One sequence of 4096 tokens and one kv head: 10.5 us,
-// a chain of lookups, one copy, one tile and two merges.
+// Measured on B200: 4-bit, 4 sequences of 128K, 32 query / 4 kv heads, d = 128 (302 MB): 81 us, 3.7 TB/s.  60 % of the
+// issue slots and 52 % of the ALU pipe are used; 15 warps per SM do not hide the chain of the unpacking (about 630
+// instructions per 32 tokens and 8 heads), and copying alone takes 66 us with the start and the merge, 20 above the
+// bytes' time.  bf16, 64K: 94 us, 5.7 TB/s; bound by memory.  One sequence of 4096 tokens and one kv head: 10.8 us, a
+// chain of lookups, one copy, one tile and two merges.
 #include "paged.cuh"
 #include "warp_mma.cuh"
 

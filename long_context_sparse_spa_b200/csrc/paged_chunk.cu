@@ -28,12 +28,13 @@
 // unit merges its shares in the order of the CTAs.
 //
 // Measured on B200, 1024 new tokens at 28672, 32 query / 8 kv heads, d = 128 (472 GFLOP; 293 us at the measured
-// bf16 rate): 667 us, 708 TFLOP/s.  It is bound by the chain of one row tile (about 6300 clocks per 128 tokens:
-// products 1500, exponentials 2050 at 16 a clock for both row tiles together, TMEM reads and barriers); without the
-// exponentials the same kernel takes 426 us, without the unpacking 577, with one product in eight 518.  Steps that
-// counted: four to eight unpacking warps 1128 -> 892, the weights' product not waiting for the next keys -> 805,
-// loops over 32 columns kept rolled (the roles share the instruction cache) -> 666.  The same from bf16 pages
-// (708 GFLOP with the weights' two parts, 439 us at that rate): 711 us, where the mma.sync kernel takes 3282.
+// bf16 rate): 662 us, 713 TFLOP/s.  It is bound by the chain of one row tile (about 6300 clocks per 128 tokens:
+// products 1500, exponentials 2050 at 16 a clock for both row tiles together, TMEM reads and barriers): the tensor pipe
+// is used 34 % of the time, the issue slots 51 %.  When the kernel took 667 us it took 426 without the exponentials, 577
+// without the unpacking, 518 with one product in eight.  Steps that counted: four to eight unpacking warps 1128 -> 892,
+// the weights' product not waiting for the next keys -> 805, loops over 32 columns kept rolled (the roles share the
+// instruction cache) -> 666.  The same from bf16 pages (708 GFLOP with the weights' two parts, 439 us at that rate):
+// 697 us, where the mma.sync kernel takes 3509.
 #include "paged.cuh"
 #include "tc.cuh"
 
@@ -612,8 +613,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_chunk_kernel(PagedAttendPar
             }
         } else if (warp == 8 + kUnpack || warp == 8 + kUnpack + 1) {
             // ================================================================ MMA issue
-            // A warp per row tile, so that neither waits for the other's weights (one warp for both: 696 us, see the file's
-            // table).  The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.
+            // A warp per row tile, so that neither waits for the other's weights (one warp for both: 696 us, where two took
+            // 667).  The whole warp runs the loop, so that descriptors stay in uniform registers; one elected lane issues.
             constexpr uint32_t kIdS = INT4 ? idesc_f16(128, kKeys, false) : idesc_bf16(128, kKeys, false);
             constexpr uint32_t kIdO = INT4 ? idesc_f16(128, D, true) : idesc_bf16(128, D, true);
             const uint64_t dq0 = sw128_desc(smem_u32(sh.q[0]), 16, 1024);
