@@ -18,9 +18,9 @@
 //   4-bit values: with 2^e the power of two of the token's largest s, r_g = s_g 2^-e and P = p 2^e, O += V^T P^T
 //     with V = (u - 8) r_g, one fp16 FMA per two codes after the AND.  V has 3 + 8 bits and is exact (a group's
 //     scale below 2^-11 of its token's largest: within 2^-19 of that); only the weight is rounded, to fp16's 11
-//     bits, half a step of the outputs' bf16 / 8.  A transposing ldmatrix over 16-bit units (four codes of a
-//     token) pairs tokens for the A operand.  So that P fits fp16 whatever the scales are, the running reference
-//     of the softmax is the maximum of (logit + e), not of the logit; P <= 2^15, and l = sum p is kept in fp32.
+//     bits, three more than the outputs have.  A transposing ldmatrix over 16-bit units (four codes of a token)
+//     pairs tokens for the A operand.  So that P fits fp16 whatever the scales are, the running reference of the
+//     softmax is the maximum of (logit + e), not of the logit; P <= 2^15, and l = sum p is kept in fp32.
 //   bf16 rows: S = K Q^T, O += V^T P^T with P = hi + lo bf16 (about 16 bits).
 // The m16 rows of a tile are a permutation of its tokens (tau) that keeps the shared-memory reads free
 // of bank conflicts for the rows' strides; a softmax does not see the order.

@@ -28,7 +28,7 @@ if not torch.cuda.is_available():
     pytest.skip("needs a CUDA device", allow_module_level=True)
 
 import long_context_sparse_spa_b200 as spa  # noqa: E402
-from test_gpu_paged import BF16, INT4, Cache, _bf, _i32, _np  # noqa: E402
+from test_gpu_paged import BF16, INT4, INVALID, Cache, _bf, _i32, _np  # noqa: E402
 
 
 def put(c, b, n, k, v):
@@ -150,3 +150,28 @@ def test_groups_of_a_token_that_lie_far_apart(d, new, span):
     for i in sorted({0, new // 2, new - 1}):
         check_closely(c, _bf(q)[i], _np(plan.out_f32)[i].astype(np.float64), _np(plan.lse)[i].astype(np.float64),
                       np.arange(400) <= 400 - new + i, 0.1, 0, f"query {i}", apart=span > 9)
+
+
+@pytest.mark.parametrize("new", [60, 5, 1])
+def test_far_scales_beside_a_missing_page_and_a_value_that_is_not_finite(new):
+    L, d, scale = 400, 128, 0.1
+    c = Cache([L], 1, d, 16, INT4, seed=65)
+    rng = np.random.default_rng(65)
+    for n in range(L):
+        big = n % 7 == 3
+        put(c, 0, n, rng.standard_normal(d) * 0.3 - 2.4 * big, rng.standard_normal(d) * (2.0**20 if big else 1.0))
+    # token 10, that every query sees: group 2 of its value; tokens 48-63: no page
+    host = c.pool.reshape(c.pool.shape[0], 1, 16, -1)
+    host[int(c.table[0, 0]), 0, 10, d + 12:d + 14] = torch.tensor([0xC0, 0x7F], dtype=torch.uint8, device="cuda")
+    c.kw["page_table"][0, 3] = -1
+    q = torch.from_numpy((1 + 0.3 * rng.standard_normal((new, 4, d))).astype(np.float32)).cuda().to(torch.bfloat16)
+    plan = spa.paged_attend(q=q, sm_scale=scale, seq_start=_i32([0, new]), want_f32=True, **c.kw)
+    assert spa.read_device_status(plan.ws) == INVALID
+    n = np.arange(L)
+    c.V[0][:, :, 64:96] = 0
+    for i in sorted({0, new // 2, new - 1}):
+        out = _np(plan.out_f32)[i].astype(np.float64)
+        assert np.isnan(out[:, 64:96]).all()
+        out[:, 64:96] = 0
+        check_closely(c, _bf(q)[i], out, _np(plan.lse)[i].astype(np.float64), (n <= L - new + i) & ((n < 48) | (n >= 64)),
+                      scale, 0, f"query {i}")
