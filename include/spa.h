@@ -102,9 +102,10 @@ const char* spa_last_cuda_error(void);
 #define SPA_TEST_STALL_PAGED_CHUNK 16
 spa_status spa_test_stall(int bits);
 
-/* ABI version of this header: 6 (spa_decode_args gained local_units in 2, the RLA fields in 3;
+/* ABI version of this header: 7 (spa_decode_args gained local_units in 2, the RLA fields in 3;
  * the min-max and mean block scores and spa_block_minmax came in 4; bf16 statistics in 5;
- * spa_select_static_status in 6). */
+ * spa_select_static_status in 6; the timed prefills in 7, and beside it, with no change of what
+ * was there, the paged KV cache). */
 int spa_abi_version(void);
 
 /* ------------------------------------------------------------------------------------
